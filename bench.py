@@ -525,8 +525,8 @@ def traffic_for(kernel: str, workload_name: str):
 
 # Sources that build the grouped expert GEMMs and their launch (tensor maps,
 # variant choice): the files a traffic figure for those kernels depends on.
-GEMM_SOURCES = ("grouped_gemm.cu", "grouped_gemm_swap.cu", "nvfp4_gemm.cu", "nvfp4_gemm_swap.cu", "gemm_common.cuh",
-                "ptx.cuh", "common.cuh", "abi.cu")
+GEMM_SOURCES = ("grouped_gemm.cu", "grouped_gemm_swap.cu", "nvfp4_gemm.cu", "nvfp4_gemm_swap.cu", "mxfp4_gemm.cu",
+                "gemm_common.cuh", "fp4.cuh", "ptx.cuh", "common.cuh", "abi.cu")
 
 
 def kernel_source_sha() -> str:

@@ -66,8 +66,12 @@ typedef struct CUstream_st* moe_stream_t;
 enum {
   MOE_WDTYPE_BF16 = 0,     /* bf16 weights, bf16 activations */
   MOE_WDTYPE_FP8_E4M3 = 1, /* E4M3 weights with 128x128 fp32 block scales, E4M3 1x128 activations */
-  MOE_WDTYPE_NVFP4 = 2     /* NVFP4 weights, bf16 activations (W4A16; see moe_weights) */
+  MOE_WDTYPE_NVFP4 = 2,    /* NVFP4 weights, bf16 activations (W4A16; see moe_weights) */
+  MOE_WDTYPE_MXFP4 = 3     /* MXFP4 weights and activations (W4A4; see moe_weights) */
 };
+
+/* Type of the plain values that the 4-bit quantiser reads and its inverse writes. */
+enum { MOE_VALUES_BF16 = 0, MOE_VALUES_F32 = 1 };
 
 /* Status codes (returned, or latched on the device). */
 enum {
@@ -91,8 +95,7 @@ typedef struct moe_config {
 } moe_config;
 
 /* Device pointers to one layer's weights (see the layouts above). Scale
- * pointers are used only for MOE_WDTYPE_FP8_E4M3 and MOE_WDTYPE_NVFP4;
- * shared-expert pointers only when n_shared == 1. router_bias may be NULL (no
+ * pointers are used for every storage but MOE_WDTYPE_BF16; shared-expert pointers only when n_shared == 1. router_bias may be NULL (no
  * bias).
  * MOE_WDTYPE_NVFP4 (TensorFold PR page: the NVFP4 format its W4A16 linears
  * read; a variant the pages describe for another model): every expert matrix
@@ -101,7 +104,12 @@ typedef struct moe_config {
  * uint8, one per 16 inputs (s1/s3/s2), and one fp32 global scale per matrix
  * (g1/g3/g2 [E]; the shared expert's sg1/sg3/sg2 [1]); an element is
  * e2m1 x e4m3 x global. Activations and h stay bf16. Needs H and I multiples
- * of 256. */
+ * of 256.
+ * MOE_WDTYPE_MXFP4 (OCP Microscaling Formats v1.0): E2M1 codes [n, k/2] as
+ * above and E8M0 scales [n, k/32] uint8, one per 32 inputs (s1/s3/s2); an
+ * element is e2m1 x 2^(byte - 127), byte 255 is NaN. x and h are quantised to
+ * the same format (moe_quantize_fp4 says how) and the products run on the
+ * block-scaled tensor core. Needs H and I multiples of 512. */
 typedef struct moe_weights {
   const void* router_w;
   const float* router_bias;
@@ -174,6 +182,34 @@ MOE_API int moe_route(const moe_config* cfg, int64_t T, const void* x, const voi
  * all-zero block gets scale 1 and zero codes). */
 MOE_API int moe_quantize_act(int64_t T, int32_t hidden, const void* x, uint8_t* q, float* s, moe_stream_t stream);
 
+/* Microscaled 4-bit storage of n_mat contiguous matrices x [n_mat, rows, k]
+ * (bf16 or fp32: x_dtype): E2M1 codes [n_mat, rows, k/2], two per byte with the
+ * even input in the low nibble, and a scale byte per block of a row's inputs.
+ *   MOE_WDTYPE_MXFP4: scales [n_mat, rows, k/32] E8M0, 2^e with e =
+ *     floor(log2(blockmax)) - 2, at least -127; an all-zero block gets scale 1;
+ *     codes = x / 2^e to the nearest E2M1 value, ties to even, saturating at 6.
+ *     k a multiple of 32; g is not used (NULL).
+ *   MOE_WDTYPE_NVFP4: scales [n_mat, rows, k/16] E4M3, s = blockmax / (6 g) to
+ *     the nearest, at most 448; codes = x / (s g) to the nearest E2M1 value, ties
+ *     to even, saturating at 6 (s = 0: zero codes). Both quotients are rounded
+ *     once. g [n_mat] fp32 (device): a global scale per matrix; k a multiple of 16.
+ * A block with an infinity or NaN, and every NVFP4 block of a matrix whose g is
+ * not positive and finite, gets the scale's NaN byte and zero codes. The sign of
+ * a value that rounds to zero is kept. x and codes 16-byte aligned. */
+MOE_API int moe_quantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x,
+                             const float* g, uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+
+/* NVFP4 global scales: g[m] = amax(x[m]) / (6 * 448), rounded once; 1 for an
+ * all-zero matrix. x as for moe_quantize_fp4, k a multiple of 16. */
+MOE_API int moe_fp4_global_scale(int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x, float* g,
+                                 moe_stream_t stream);
+
+/* The values that codes and scales stand for: y [n_mat, rows, k] = (e2m1 x
+ * scale) x g, rounded once to fp32 (MXFP4: exact in fp32) and, for y_dtype
+ * MOE_VALUES_BF16, once more to bf16. Layouts as for moe_quantize_fp4. */
+MOE_API int moe_dequantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, const uint8_t* codes,
+                               const uint8_t* scales, const float* g, int32_t y_dtype, void* y, moe_stream_t stream);
+
 /* Histogram/scan/permute of a routing decision. Groups 0..E-1 are the routed
  * experts, group E the shared expert (all T tokens) when n_shared == 1.
  *   counts  [E+S] int32    rows per group
@@ -230,8 +266,10 @@ MOE_API int moe_experts(const moe_config* cfg, int64_t T, const void* x, const i
  *                                A W1_g^T, then the up sums A W3_g^T (no SwiGLU)
  *   stage MOE_STAGE_DOWN:        A [R, I]; out = y [R, H] bf16 = row_gate[r] * (A W2_g^T)
  *                                (row_gate [R] fp32, device; NULL means 1)
- * A is bf16 (BF16 storage) or E4M3 codes with a_scale [R, K/128] fp32 (FP8, K
- * the reduction length). The workspace is moe_workspace_bytes for
+ * A is bf16 (BF16 and NVFP4 storage) or E4M3 codes with a_scale [R, K/128] fp32
+ * (FP8, K the reduction length). MXFP4: A holds codes [R, K/2] with a_scale
+ * [R, K/32] E8M0 bytes (16-byte aligned), and GATE_UP writes h in that form (out
+ * [R, I/2], out_scale [R, I/32] bytes). The workspace is moe_workspace_bytes for
  * ceil(R / (top_k + n_shared)) tokens. Device status: moe_read_status. */
 enum { MOE_STAGE_GATE_UP = 1, MOE_STAGE_GATE_UP_RAW = 2, MOE_STAGE_DOWN = 3 };
 MOE_API int moe_grouped_gemm(const moe_config* cfg, int stage, int64_t R, const int32_t* offsets, const void* a,

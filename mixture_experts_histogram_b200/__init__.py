@@ -11,7 +11,8 @@ The functions carry the names of the C entry points:
   moe_status_string, moe_profile_enable, moe_profile_read, moe_device_sm_count,
   moe_set_gemm_variant, moe_permute_noalloc, moe_rmsnorm, moe_combine_residual,
   moe_grouped_gemm, moe_read_status_detail, moe_debug_inject, moe_launch_count,
-  moe_forward_ep_partial, moe_ep_reduce.
+  moe_forward_ep_partial, moe_ep_reduce, moe_quantize_fp4, moe_fp4_global_scale,
+  moe_dequantize_fp4.
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ from typing import Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_b200.so")
 
-MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3, MOE_WDTYPE_NVFP4 = 0, 1, 2
+MOE_WDTYPE_BF16, MOE_WDTYPE_FP8_E4M3, MOE_WDTYPE_NVFP4, MOE_WDTYPE_MXFP4 = 0, 1, 2, 3
+MOE_VALUES_BF16, MOE_VALUES_F32 = 0, 1
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
 MOE_ERR_UNSUPPORTED_SHAPE = 2
@@ -74,6 +76,9 @@ def load():
         "moe_forward_host_async": [cfgp, i64, vp, wp, vp, vp, sz, vp],
         "moe_route": [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_quantize_act": [i64, i32, vp, vp, vp, vp],
+        "moe_quantize_fp4": [i32, i64, i64, i32, i32, vp, vp, vp, vp, vp],
+        "moe_fp4_global_scale": [i64, i64, i32, i32, vp, vp, vp],
+        "moe_dequantize_fp4": [i32, i64, i64, i32, vp, vp, vp, i32, vp, vp],
         "moe_permute": [cfgp, i64, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_experts": [cfgp, i64, vp, vp, vp, wp, vp, vp, vp, sz, vp],
         "moe_combine": [cfgp, i64, vp, vp, vp, vp],
@@ -174,6 +179,32 @@ def moe_route(cfg, T, x, router_w, router_bias, topk_idx, topk_w, logits, worksp
 
 def moe_quantize_act(T, hidden, x, q, s, stream=None):
     _check(load().moe_quantize_act(T, hidden, _ptr(x), _ptr(q), _ptr(s), _stream(stream)), "moe_quantize_act")
+
+
+def _values_dtype(t) -> int:
+    """MOE_VALUES_* of a tensor of plain values."""
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"values must be bfloat16 or float32, not {t.dtype}")
+    return MOE_VALUES_F32 if t.dtype == torch.float32 else MOE_VALUES_BF16
+
+
+def moe_quantize_fp4(fmt, n_mat, rows, k, x, g, codes, scales, stream=None):
+    """n_mat matrices x [n_mat, rows, k] (bf16 or fp32) to MXFP4 (g None) or NVFP4 codes and scales."""
+    _check(load().moe_quantize_fp4(fmt, n_mat, rows, k, _values_dtype(x), _ptr(x), _ptr(g), _ptr(codes),
+                                   _ptr(scales), _stream(stream)), "moe_quantize_fp4")
+
+
+def moe_fp4_global_scale(n_mat, rows, k, x, g, stream=None):
+    """NVFP4 global scale of each matrix: g[m] = amax(x[m]) / (6 * 448)."""
+    _check(load().moe_fp4_global_scale(n_mat, rows, k, _values_dtype(x), _ptr(x), _ptr(g), _stream(stream)),
+           "moe_fp4_global_scale")
+
+
+def moe_dequantize_fp4(fmt, n_mat, rows, k, codes, scales, g, y, stream=None):
+    """The values y [n_mat, rows, k] (bf16 or fp32) that codes and scales stand for."""
+    _check(load().moe_dequantize_fp4(fmt, n_mat, rows, k, _ptr(codes), _ptr(scales), _ptr(g), _values_dtype(y),
+                                     _ptr(y), _stream(stream)), "moe_dequantize_fp4")
 
 
 def moe_permute(cfg, T, topk_idx, counts, offsets, perm, pos, workspace, stream=None):

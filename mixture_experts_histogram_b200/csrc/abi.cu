@@ -39,9 +39,9 @@ constexpr int kStoreYMaxInter = 4096;
 // tile's K range is split so that about one item runs per SM, every piece at
 // least 4 K stages deep, and the pieces' fp32 sums are added afterwards in
 // piece order. A function of the configuration and R only (it also sizes the
-// workspace); NVFP4 does not split.
+// workspace); NVFP4 and MXFP4 do not split.
 int down_k_split(const moe_config& c, int64_t R) {
-  if (c.wdtype == MOE_WDTYPE_NVFP4 || R <= 0) return 1;
+  if (c.wdtype == MOE_WDTYPE_NVFP4 || c.wdtype == MOE_WDTYPE_MXFP4 || R <= 0) return 1;
   const int64_t groups = c.n_experts + c.n_shared;
   const int64_t items = ((groups < R ? groups : R) + R / kTileM) * ceil_div(c.hidden, 256);
   if (2 * items > kRouterTargetCtas) return 1;
@@ -102,11 +102,14 @@ int check_config(const moe_config* c, int64_t T) {
   if (T < 0) return MOE_ERR_INVALID_ARG;
   if (c->hidden <= 0 || c->inter <= 0 || c->n_experts <= 0 || c->top_k <= 0) return MOE_ERR_INVALID_ARG;
   if (c->n_shared < 0 || c->n_shared > 1) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (c->wdtype != MOE_WDTYPE_BF16 && c->wdtype != MOE_WDTYPE_FP8_E4M3 && c->wdtype != MOE_WDTYPE_NVFP4)
+  if (c->wdtype != MOE_WDTYPE_BF16 && c->wdtype != MOE_WDTYPE_FP8_E4M3 && c->wdtype != MOE_WDTYPE_NVFP4 &&
+      c->wdtype != MOE_WDTYPE_MXFP4)
     return MOE_ERR_INVALID_ARG;
   if (c->hidden % 128 || c->inter % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
   // NVFP4: the scale tensors' rows (K/16 bytes) must be whole 16-byte TMA strides.
   if (c->wdtype == MOE_WDTYPE_NVFP4 && (c->hidden % 256 || c->inter % 256)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // MXFP4: the same of K/32-byte rows.
+  if (c->wdtype == MOE_WDTYPE_MXFP4 && (c->hidden % 512 || c->inter % 512)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (c->n_experts > kMaxExperts || c->top_k > kMaxTopK || c->top_k > c->n_experts) return MOE_ERR_UNSUPPORTED_SHAPE;
   if ((int64_t)(c->top_k + c->n_shared) * T >= ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED_SHAPE;
   if ((int64_t)c->n_experts * c->hidden >= ((int64_t)1 << 31) || (int64_t)c->n_experts * c->inter >= ((int64_t)1 << 31))
@@ -118,23 +121,24 @@ int check_weights(const moe_config* c, const moe_weights* w) {
   if (!w) return MOE_ERR_INVALID_ARG;
   const bool fp8 = c->wdtype == MOE_WDTYPE_FP8_E4M3;
   const bool nv = c->wdtype == MOE_WDTYPE_NVFP4;
+  const bool mx = c->wdtype == MOE_WDTYPE_MXFP4;
   const void* need[] = {w->router_w, w->w1, w->w3, w->w2};
   for (const void* p : need) {
     if (!p) return MOE_ERR_INVALID_ARG;
     if (!aligned(p, 16)) return MOE_ERR_MISALIGNED;
   }
-  if ((fp8 || nv) && (!w->s1 || !w->s3 || !w->s2)) return MOE_ERR_INVALID_ARG;
+  if ((fp8 || nv || mx) && (!w->s1 || !w->s3 || !w->s2)) return MOE_ERR_INVALID_ARG;
   if (nv && (!w->g1 || !w->g3 || !w->g2)) return MOE_ERR_INVALID_ARG;
-  if (nv && (!aligned(w->s1, 16) || !aligned(w->s3, 16) || !aligned(w->s2, 16))) return MOE_ERR_MISALIGNED;
+  if ((nv || mx) && (!aligned(w->s1, 16) || !aligned(w->s3, 16) || !aligned(w->s2, 16))) return MOE_ERR_MISALIGNED;
   if (c->n_shared) {
     const void* sh[] = {w->sw1, w->sw3, w->sw2};
     for (const void* p : sh) {
       if (!p) return MOE_ERR_INVALID_ARG;
       if (!aligned(p, 16)) return MOE_ERR_MISALIGNED;
     }
-    if ((fp8 || nv) && (!w->ss1 || !w->ss3 || !w->ss2)) return MOE_ERR_INVALID_ARG;
+    if ((fp8 || nv || mx) && (!w->ss1 || !w->ss3 || !w->ss2)) return MOE_ERR_INVALID_ARG;
     if (nv && (!w->sg1 || !w->sg3 || !w->sg2)) return MOE_ERR_INVALID_ARG;
-    if (nv && (!aligned(w->ss1, 16) || !aligned(w->ss3, 16) || !aligned(w->ss2, 16))) return MOE_ERR_MISALIGNED;
+    if ((nv || mx) && (!aligned(w->ss1, 16) || !aligned(w->ss3, 16) || !aligned(w->ss2, 16))) return MOE_ERR_MISALIGNED;
   }
   return MOE_OK;
 }
@@ -301,6 +305,7 @@ enum GemmKind { kSingle = 0, kPair = 1, kSwap = 2 };
 GemmKind gemm_kind(bool gate_up, int64_t routed_rows, int n_experts, int wdtype) {
   const bool fp8 = wdtype == MOE_WDTYPE_FP8_E4M3;
   const bool nvfp4 = wdtype == MOE_WDTYPE_NVFP4;
+  if (wdtype == MOE_WDTYPE_MXFP4) return kSingle;  // one kernel for every group size
   switch (g_gemm_variant) {
     case MOE_GEMM_SINGLE: return kSingle;
     case MOE_GEMM_PAIR: return nvfp4 ? kSingle : kPair;
@@ -319,15 +324,68 @@ bool amaps(AMaps* a, const void* base, bool fp8, uint64_t inner, uint64_t rows) 
          map_2d(&a->rows64, base, fp8, inner, rows, box_k, 64) && map_2d(&a->rows32, base, fp8, inner, rows, box_k, 32);
 }
 
+// Both MXFP4 GEMMs (mxfp4_gemm.cu) over R rows of codes A [R, K/2] with E8M0
+// scales a_scale [R, K/32]: gate/up (out = h codes [R, I/2] and out_scale [R,
+// I/32], or fp32 sums if raw) or down (out = y [R, H] bf16).
+int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, int64_t R, const void* a, const void* a_scale,
+              const int32_t* offsets, const int32_t* mt, const moe_weights* w, const float* row_gate, void* out,
+              void* out_scale, bool raw, int* status, cudaStream_t s) {
+  const int E = c->n_experts, S = c->n_shared;
+  const uint64_t K = gate_up ? c->hidden : c->inter, N = gate_up ? c->inter : c->hidden;
+  const uint32_t box = gate_up ? 128 : 256;
+  const int sms = sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  AMaps ma;
+  MxMaps m;
+  auto weights = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows) {
+    return map_2d(code, cp, true, K / 2, rows, kStageBytesK, box) && map_u8(scale, sp, K / 32, rows, 16, box);
+  };
+  bool ok = amaps(&ma, a, true, K / 2, R) && map_u8(&m.a_scale, a_scale, K / 32, R, 16, kTileM) &&
+            weights(&m.code0, &m.scale0, gate_up ? w->w1 : w->w2, gate_up ? w->s1 : w->s2, E * N);
+  if (S) ok = ok && weights(&m.scode0, &m.sscale0, gate_up ? w->sw1 : w->sw2, gate_up ? w->ss1 : w->ss2, N);
+  else m.scode0 = m.code0, m.sscale0 = m.scale0;
+  if (gate_up) {
+    ok = ok && weights(&m.code1, &m.scale1, w->w3, w->s3, E * N);
+    if (S) ok = ok && weights(&m.scode1, &m.sscale1, w->sw3, w->ss3, N);
+    else m.scode1 = m.code1, m.sscale1 = m.scale1;
+  } else {
+    m.code1 = m.code0, m.scale1 = m.scale0, m.scode1 = m.scode0, m.sscale1 = m.sscale0;
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  GemmParams g{};
+  g.k_split = 1;
+  g.mt_prefix = mt;
+  g.offsets = offsets;
+  g.G = E + S;
+  g.E = E;
+  g.K = (int32_t)K;
+  g.N = (int32_t)N;
+  g.n_tiles = (int32_t)(N / box);
+  g.n_fastest = gate_up ? 0 : 1;
+  g.R = (int32_t)R;
+  g.rows_pad = L.rows_pad;
+  g.out = out;
+  g.out_scale = static_cast<float*>(out_scale);
+  g.row_gate = row_gate;
+  g.status = status;
+  g.wait_ns = g_wait_ns;
+  g.raw_out = raw ? 1 : 0;
+  g.inject = g_inject;
+  CUDA_TRY(launch_mxfp4_gemm(g, gate_up, sms, ma, m, s));
+  return MOE_OK;
+}
+
 // The grouped gate/up GEMM (GEMM1) over R rows of A [R, H] grouped by `offsets`
 // (tile prefixes mt / mp for single CTAs / pairs). FP8: a_scale_t [H/128,
 // rows_pad]; out = h codes [R, I] with out_scale_t [I/128, rows_pad]. BF16: out
-// = h [R, I] bf16. raw: out = fp32 [R, 2I] gate and up sums (no SwiGLU).
+// = h [R, I] bf16. MXFP4: see run_mxfp4 (row-major scales). raw: out = fp32 [R, 2I] gate and up sums (no SwiGLU).
 int run_gate_up(const moe_config* c, const WsLayout& L, int64_t R, const void* a, const float* a_scale_t,
                 const int32_t* offsets, const int32_t* mt, const int32_t* mp, GemmKind kind, const moe_weights* w,
                 void* out, float* out_scale_t, bool raw, int* status, cudaStream_t s) {
   const bool pair = kind == kPair;
   if (!get_encoder()) return MOE_ERR_CUDA;
+  if (c->wdtype == MOE_WDTYPE_MXFP4)
+    return run_mxfp4(c, L, true, R, a, a_scale_t, offsets, mt, w, nullptr, out, out_scale_t, raw, status, s);
   const bool fp8 = c->wdtype == MOE_WDTYPE_FP8_E4M3;
   const int H = c->hidden, I = c->inter, E = c->n_experts, S = c->n_shared;
   const uint32_t box_k = fp8 ? 128 : 64;
@@ -422,6 +480,8 @@ int run_down(const moe_config* c, const WsLayout& L, int64_t R, const void* a, c
              const float* row_gate, void* y, uint8_t* ws, int* status, cudaStream_t s) {
   const bool pair = kind == kPair;
   if (!get_encoder()) return MOE_ERR_CUDA;
+  if (c->wdtype == MOE_WDTYPE_MXFP4)
+    return run_mxfp4(c, L, false, R, a, a_scale_t, offsets, mt, w, row_gate, y, nullptr, false, status, s);
   const bool fp8 = c->wdtype == MOE_WDTYPE_FP8_E4M3;
   const int H = c->hidden, I = c->inter, E = c->n_experts, S = c->n_shared;
   const uint32_t box_k = fp8 ? 128 : 64;
@@ -539,9 +599,10 @@ int run_experts(const moe_config* c, const WsLayout& L, int64_t T, const void* x
   gp.x = static_cast<const uint16_t*>(x);
   gp.pos = pos;
   gp.xp = ws + L.xp;
-  gp.sxp = fp8 ? reinterpret_cast<float*>(ws + L.sxp) : nullptr;
+  const bool mx = c->wdtype == MOE_WDTYPE_MXFP4;
+  gp.sxp = fp8 || mx ? reinterpret_cast<float*>(ws + L.sxp) : nullptr;
   gp.scale_row_major = 0;
-  CUDA_TRY(launch_gather(gp, fp8, s));
+  CUDA_TRY(mx ? launch_gather_mx(gp, s) : launch_gather(gp, fp8, s));
   prof.mark();
 
   const int32_t* offsets = reinterpret_cast<const int32_t*>(ws + L.offsets);
@@ -596,7 +657,9 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   WsLayout L{};
   const int S = c.n_shared, k = c.top_k, E = c.n_experts, G = E + S;
   const bool fp8 = c.wdtype == MOE_WDTYPE_FP8_E4M3;
-  const int64_t es = fp8 ? 1 : 2;
+  const bool mx = c.wdtype == MOE_WDTYPE_MXFP4;
+  // Bytes of two activation values.
+  const int64_t es2 = mx ? 1 : fp8 ? 2 : 4;
   L.T = T;
   L.R = (int64_t)(k + S) * T;
   L.rows_pad = round_up(L.R, kTileM) + 2 * kTileM;  // a 256-row pair tile may start at the last row
@@ -623,10 +686,11 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   L.perm = take((size_t)L.R * 4);
   L.pos = take((size_t)T * (k + S) * 4);
   L.row_gate = take((size_t)L.R * 4);
-  L.xp = take((size_t)L.R * c.hidden * es);
-  L.sxp = take(fp8 ? (size_t)(c.hidden / 128) * L.rows_pad * 4 : 0);
-  L.h = take((size_t)L.R * c.inter * es);
-  L.sh = take(fp8 ? (size_t)(c.inter / 128) * L.rows_pad * 4 : 0);
+  auto scales = [&](int64_t K) { return fp8 ? (K / 128) * L.rows_pad * 4 : mx ? L.R * (K / 32) : 0; };
+  L.xp = take((size_t)L.R * c.hidden * es2 / 2);
+  L.sxp = take((size_t)scales(c.hidden));
+  L.h = take((size_t)L.R * c.inter * es2 / 2);
+  L.sh = take((size_t)scales(c.inter));
   L.y = take((size_t)L.R * c.hidden * 2);
   const int k2 = down_k_split(c, L.R);
   L.part = take(k2 > 1 ? (size_t)k2 * L.R * c.hidden * 4 : 0);
@@ -774,6 +838,57 @@ int moe_quantize_act(int64_t T, int32_t hidden, const void* x, uint8_t* q, float
   return MOE_OK;
 }
 
+// Arguments common to the microscaled 4-bit entry points; *elems = values per matrix.
+static int check_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x,
+                     int64_t* elems) {
+  const bool mx = format == MOE_WDTYPE_MXFP4;
+  if (!mx && format != MOE_WDTYPE_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (x_dtype != MOE_VALUES_BF16 && x_dtype != MOE_VALUES_F32) return MOE_ERR_INVALID_ARG;
+  if (n_mat < 0 || rows < 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+  if (k % (mx ? 32 : 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  constexpr int64_t kMost = (int64_t)1 << 40;
+  if (rows > kMost / k || (rows && n_mat > kMost / (rows * k))) return MOE_ERR_UNSUPPORTED_SHAPE;
+  *elems = rows * k;
+  if (n_mat * *elems == 0) return MOE_OK;
+  if (!x) return MOE_ERR_INVALID_ARG;
+  return aligned(x, 16) ? MOE_OK : MOE_ERR_MISALIGNED;
+}
+
+int moe_quantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x,
+                     const float* g, uint8_t* codes, uint8_t* scales, moe_stream_t stream) {
+  int64_t elems = 0;
+  const int rc = check_fp4(format, n_mat, rows, k, x_dtype, x, &elems);
+  if (rc != MOE_OK || n_mat * elems == 0) return rc;
+  if (!codes || !scales || (format == MOE_WDTYPE_NVFP4 && !g)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || (g && !aligned(g, 4))) return MOE_ERR_MISALIGNED;
+  CUDA_TRY(launch_quantize_fp4(format == MOE_WDTYPE_MXFP4, x_dtype == MOE_VALUES_F32, n_mat, elems, x, g, codes, scales,
+                               reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_fp4_global_scale(int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x, float* g,
+                         moe_stream_t stream) {
+  int64_t elems = 0;
+  const int rc = check_fp4(MOE_WDTYPE_NVFP4, n_mat, rows, k, x_dtype, x, &elems);
+  if (rc != MOE_OK || n_mat * elems == 0) return rc;
+  if (!g) return MOE_ERR_INVALID_ARG;
+  if (!aligned(g, 4)) return MOE_ERR_MISALIGNED;
+  CUDA_TRY(launch_fp4_global_scale(x_dtype == MOE_VALUES_F32, n_mat, elems, x, g, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_dequantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, const uint8_t* codes,
+                       const uint8_t* scales, const float* g, int32_t y_dtype, void* y, moe_stream_t stream) {
+  int64_t elems = 0;
+  const int rc = check_fp4(format, n_mat, rows, k, y_dtype, y, &elems);
+  if (rc != MOE_OK || n_mat * elems == 0) return rc;
+  if (!codes || !scales || (format == MOE_WDTYPE_NVFP4 && !g)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || (g && !aligned(g, 4))) return MOE_ERR_MISALIGNED;
+  CUDA_TRY(launch_dequantize_fp4(format == MOE_WDTYPE_MXFP4, y_dtype == MOE_VALUES_F32, n_mat, elems, codes, scales, g,
+                                 y, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
 int moe_permute(const moe_config* cfg, int64_t T, const int32_t* topk_idx, int32_t* counts, int32_t* offsets,
                 int32_t* perm, int32_t* pos, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   int rc = check_config(cfg, T);
@@ -844,8 +959,10 @@ int moe_grouped_gemm(const moe_config* cfg, int stage, int64_t R, const int32_t*
   if (R < 0 || !offsets || !a || !out) return MOE_ERR_INVALID_ARG;
   if (R >= ((int64_t)1 << 31) - 512) return MOE_ERR_UNSUPPORTED_SHAPE;
   const bool fp8 = cfg->wdtype == MOE_WDTYPE_FP8_E4M3;
-  if (fp8 && !a_scale) return MOE_ERR_INVALID_ARG;
-  if (fp8 && stage == MOE_STAGE_GATE_UP && !out_scale) return MOE_ERR_INVALID_ARG;
+  const bool mx = cfg->wdtype == MOE_WDTYPE_MXFP4;
+  if ((fp8 || mx) && !a_scale) return MOE_ERR_INVALID_ARG;
+  if ((fp8 || mx) && stage == MOE_STAGE_GATE_UP && !out_scale) return MOE_ERR_INVALID_ARG;
+  if (mx && !aligned(a_scale, 16)) return MOE_ERR_MISALIGNED;
   if (!aligned(a, 16) || !aligned(out, 16) || !aligned(offsets, 4)) return MOE_ERR_MISALIGNED;
   // The workspace of moe_forward for ceil(R / (top_k + n_shared)) tokens holds
   // every scratch buffer this needs.
@@ -863,14 +980,14 @@ int moe_grouped_gemm(const moe_config* cfg, int stage, int64_t R, const int32_t*
   int32_t* mp = reinterpret_cast<int32_t*>(ws + L.mp_prefix);
   CUDA_TRY(launch_tile_prefix(offsets, G, (int32_t)R, mt, mp, status, s));
   if (stage == MOE_STAGE_DOWN) {
-    float* a_t = reinterpret_cast<float*>(ws + L.sh);
-    if (fp8) CUDA_TRY(launch_scale_transpose(a_scale, a_t, R, cfg->inter / 128, L.rows_pad, true, s));
+    const float* a_t = mx ? a_scale : reinterpret_cast<const float*>(ws + L.sh);
+    if (fp8) CUDA_TRY(launch_scale_transpose(a_scale, reinterpret_cast<float*>(ws + L.sh), R, cfg->inter / 128, L.rows_pad, true, s));
     return run_down(cfg, L, R, a, a_t, offsets, mt, mp, gemm_kind(false, R, G, cfg->wdtype), w, row_gate, out, ws,
                     status, s);
   }
-  float* a_t = reinterpret_cast<float*>(ws + L.sxp);
-  float* o_t = reinterpret_cast<float*>(ws + L.sh);
-  if (fp8) CUDA_TRY(launch_scale_transpose(a_scale, a_t, R, cfg->hidden / 128, L.rows_pad, true, s));
+  const float* a_t = mx ? a_scale : reinterpret_cast<const float*>(ws + L.sxp);
+  float* o_t = mx ? out_scale : reinterpret_cast<float*>(ws + L.sh);
+  if (fp8) CUDA_TRY(launch_scale_transpose(a_scale, reinterpret_cast<float*>(ws + L.sxp), R, cfg->hidden / 128, L.rows_pad, true, s));
   const bool raw = stage == MOE_STAGE_GATE_UP_RAW;
   rc = run_gate_up(cfg, L, R, a, a_t, offsets, mt, mp, gemm_kind(true, R, G, cfg->wdtype), w, out, o_t, raw, status,
                    s);

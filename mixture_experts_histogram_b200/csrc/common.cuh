@@ -193,6 +193,30 @@ struct NvMaps {
 cudaError_t launch_nvfp4_gemm(const GemmParams& p, bool gemm1, int grid, const AMaps& tm_a, const NvMaps& tm,
                               cudaStream_t s);
 
+// MXFP4 maps of one grouped GEMM (uint8): E2M1 codes [rows, K/2] with 128-byte
+// boxes (128B swizzle, one 256-deep K stage) and E8M0 scales [rows, K/32] with
+// 16-byte boxes (two stages), activations' scales in 128-row boxes; the weight
+// maps as in NvMaps.
+struct MxMaps {
+  CUtensorMap code0, code1, scode0, scode1, scale0, scale1, sscale0, sscale1, a_scale;
+};
+
+// MXFP4 grouped GEMM on the block-scaled tensor core: GEMM1 (gate/up + SwiGLU;
+// out = h codes [R, N/2], out_scale = E8M0 bytes [R, N/32]) or GEMM2 (down, bf16
+// y). tm_a maps the activation codes.
+cudaError_t launch_mxfp4_gemm(const GemmParams& p, bool gemm1, int grid, const AMaps& tm_a, const MxMaps& tm,
+                              cudaStream_t s);
+
+// Microscaled 4-bit storage (fp4_quantize.cu): n_mat contiguous matrices of
+// `elems` values. mx: MXFP4, else NVFP4 with g [n_mat]; f32: fp32 values, else bf16.
+cudaError_t launch_quantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems, const void* x, const float* g,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_fp4_global_scale(bool f32, int64_t n_mat, int64_t elems, const void* x, float* g, cudaStream_t s);
+cudaError_t launch_dequantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems, const uint8_t* codes,
+                                  const uint8_t* scales, const float* g, void* y, cudaStream_t s);
+// The gather with MXFP4 quantisation: p.xp codes [rows, H/2], p.sxp E8M0 bytes [rows, H/32].
+cudaError_t launch_gather_mx(const GatherParams& p, cudaStream_t s);
+
 cudaError_t launch_gemm1(const GemmParams& p, bool fp8, bool pair, int grid, const AMaps& tm_a,
                          const CUtensorMap& tm_w1, const CUtensorMap& tm_w3, const CUtensorMap& tm_sw1,
                          const CUtensorMap& tm_sw3, cudaStream_t s);

@@ -1,0 +1,262 @@
+"""Microscaled 4-bit storage on the GPU: the quantisers, their inverse, and the
+MXFP4 expert GEMMs, against the plain 64-bit definitions of fp4_ref.
+
+The quantisers are correctly rounded, so codes and scale bytes must be equal.
+The GEMMs get exact cases first: E2M1 codes with power-of-two scales of a small
+range make every product and partial sum an exact fp32 number, so the sums (and
+the bf16 output) must equal the definition bit for bit; this pins the nibble
+order, the scale layout and both K halves of a scale column. The layer is held
+to the tolerance of BF16 outputs, 1e-2 (relative Frobenius, pooled and per token).
+"""
+import numpy as np
+import pytest
+
+import fp4_ref as ref
+import oracle
+import synth
+from conftest import cuda_available
+from parity import bf16_bits_to_f64, check_routing, frob_rel, rows_rel, unique_tokens
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="needs a CUDA device")]
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_histogram_b200 as mm
+    from mixture_experts_histogram_b200 import build
+    build.build()
+    mm.load()
+    return mm
+
+
+def _values(seed, n, rows, k, kind):
+    """Inputs as fp32 (bf16-representable for kind bf16): normal values, a matrix of ties,
+    blocks of zeros, tiny and huge blocks."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((n, rows, k)).astype(np.float32) * 2.0 ** rng.integers(-20, 20, (n, rows, 1)).astype(np.float32)
+    x[0] = rng.integers(-28, 29, (rows, k)) * 0.25          # every midpoint of the code grid
+    if rows > 1:
+        x[-1, 1] = 0.0
+        x[-1, 0, :16] = -0.0
+    if rows > 2:
+        x[0, 2] = x[0, 2] * np.float32(2.0 ** -130)         # below the smallest E8M0 scale
+    if rows > 3:
+        x[-1, 3] = np.sign(x[-1, 3]) * np.float32(3.0e38)
+    if kind == "bf16":
+        x = synth.bf16_to_f32(synth.f32_to_bf16(np.clip(x, -3.3e38, 3.3e38)))
+    return x
+
+
+def _tensor(x, kind):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t.to(torch.bfloat16) if kind == "bf16" else t
+
+
+SIZES = [(1, 1, 32), (1, 3, 64), (3, 5, 96), (2, 7, 4096), (5, 33, 1536), (1, 700, 512)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,k", SIZES)
+def test_mxfp4_quantize_exact(m, n, rows, k, kind):
+    import torch
+    x = _values(1, n, rows, k, kind)
+    codes = torch.full((n * rows * k // 2 + 16,), 0xAA, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n * rows * k // 32 + 16,), 0xAA, dtype=torch.uint8, device="cuda")
+    m.moe_quantize_fp4(m.MOE_WDTYPE_MXFP4, n, rows, k, _tensor(x, kind), None, codes, scales)
+    c, s = ref.mx_quantize(x)
+    assert np.array_equal(scales.cpu().numpy()[:-16], s.ravel())
+    assert np.array_equal(codes.cpu().numpy()[:-16], c.ravel())
+    assert (codes[-16:] == 0xAA).all() and (scales[-16:] == 0xAA).all()  # nothing behind the end
+    y = torch.empty((n, rows, k), dtype=torch.float32, device="cuda")
+    m.moe_dequantize_fp4(m.MOE_WDTYPE_MXFP4, n, rows, k, codes, scales, None, y)
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), ref.mx_values(c, s))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,k", [(1, 1, 16), (3, 5, 48)] + SIZES[2:])
+def test_nvfp4_quantize_exact(m, n, rows, k, kind):
+    import torch
+    x = _values(2, n, rows, k, kind)
+    if rows > 3:
+        x[-1, 3] = 1.0  # (a matrix with 3e38 would have only zeros beside it)
+    xt = _tensor(x, kind)
+    g = torch.empty(n, dtype=torch.float32, device="cuda")
+    m.moe_fp4_global_scale(n, rows, k, xt, g)
+    amax = np.abs(x).max((1, 2))
+    want_g = np.where(amax > 0, amax / np.float32(2688), np.float32(1)).astype(np.float32)
+    assert np.array_equal(g.cpu().numpy(), want_g)
+    codes = torch.empty((n, rows, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n, rows, k // 16), dtype=torch.uint8, device="cuda")
+    y = torch.empty((n, rows, k), dtype=torch.float32, device="cuda")
+    # the matrix's own scale, a power of two (ties everywhere) and one that saturates
+    for gs in (want_g, np.full(n, 2.0 ** -6, np.float32), want_g / np.float32(40)):
+        m.moe_quantize_fp4(m.MOE_WDTYPE_NVFP4, n, rows, k, xt, m.to_device(gs), codes, scales)
+        c, s = ref.nv_quantize(x, gs)
+        assert np.array_equal(scales.cpu().numpy(), s)
+        assert np.array_equal(codes.cpu().numpy(), c)
+        m.moe_dequantize_fp4(m.MOE_WDTYPE_NVFP4, n, rows, k, codes, scales, m.to_device(gs), y)
+        assert np.array_equal(y.cpu().numpy(), ref.nv_values(c, s, gs).astype(np.float32))  # one rounding
+
+
+def test_quantize_non_finite_and_bf16_output(m):
+    """A block with an infinity or NaN gets the NaN scale and zero codes; its neighbours do not change."""
+    import torch
+    x = np.random.default_rng(3).standard_normal((1, 2, 128)).astype(np.float32)
+    x[0, 0, 5], x[0, 0, 40], x[0, 1, 127] = np.inf, np.nan, -np.inf
+    x = synth.bf16_to_f32(synth.f32_to_bf16(np.where(np.isfinite(x), x, 0)) ) + np.where(np.isfinite(x), 0, x)
+    xt = torch.from_numpy(x).cuda().to(torch.bfloat16)
+    for fmt, blk in ((m.MOE_WDTYPE_MXFP4, 32), (m.MOE_WDTYPE_NVFP4, 16)):
+        g = None if fmt == m.MOE_WDTYPE_MXFP4 else torch.full((1,), 0.01, device="cuda")
+        codes = torch.empty((1, 2, 64), dtype=torch.uint8, device="cuda")
+        scales = torch.empty((1, 2, 128 // blk), dtype=torch.uint8, device="cuda")
+        m.moe_quantize_fp4(fmt, 1, 2, 128, xt, g, codes, scales)
+        c, s = ref.mx_quantize(x) if g is None else ref.nv_quantize(x, g.cpu().numpy())
+        assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), c)
+        y = torch.empty((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+        m.moe_dequantize_fp4(fmt, 1, 2, 128, codes, scales, g, y)
+        want = ref.mx_values(c, s) if g is None else ref.nv_values(c, s, g.cpu().numpy())
+        got = y.float().cpu().numpy()
+        nan = np.isnan(want)
+        assert nan.sum() == 3 * blk and np.array_equal(np.isnan(got), nan)
+        assert np.array_equal(got[~nan], synth.bf16_to_f32(synth.f32_to_bf16(want[~nan].astype(np.float32))))
+    bad = torch.tensor([float("nan")], device="cuda")
+    m.moe_quantize_fp4(m.MOE_WDTYPE_NVFP4, 1, 2, 128, xt, bad, codes, scales)
+    assert (scales == 0x7F).all() and (codes == 0).all()
+
+
+# ------------------------------------------------------------ grouped GEMMs --
+
+H, I, E = 1024, 512, 5
+COUNTS = [0, 1, 129, 300, 64, 200]  # the shared expert last
+
+
+def _matrices(seed, G, rows, cols, spread=2):
+    """Random E2M1 codes with E8M0 scales 2^-spread .. 2^spread, and their values."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (G, rows, cols // 2), dtype=np.uint8)
+    scales = (127 + rng.integers(-spread, spread + 1, (G, rows, cols // 32))).astype(np.uint8)
+    return codes, scales, ref.mx_values(codes, scales)
+
+
+def _setup(m):
+    import torch
+    cfg = m.make_config(H, E, 2, 1, I, m.MOE_WDTYPE_MXFP4)
+    mats = {"1": _matrices(1, E + 1, I, H), "3": _matrices(2, E + 1, I, H), "2": _matrices(3, E + 1, H, I)}
+    host = {"router_w": synth.normal_bf16(0, 1, (E, H), 0.05)}
+    for n, (c, s, _) in mats.items():
+        host["w" + n], host["s" + n], host["sw" + n], host["ss" + n] = c[:E], s[:E], c[E:], s[E:]
+    dev = m.upload_weights({k: np.ascontiguousarray(v) for k, v in host.items()})
+    offsets = np.concatenate([[0], np.cumsum(COUNTS)]).astype(np.int32)
+    R = int(offsets[-1])
+    ws = torch.empty(m.moe_workspace_bytes(cfg, -(-R // 3)), dtype=torch.uint8, device="cuda")
+    return cfg, dev, {n: v for n, (_, _, v) in mats.items()}, offsets, R, np.repeat(np.arange(E + 1), COUNTS), ws
+
+
+def test_mxfp4_gate_up_exact(m):
+    import torch
+    cfg, dev, w, offsets, R, group, ws = _setup(m)
+    ac, asc, a = _matrices(4, 1, R, H)
+    out = torch.full((R + 1, 2, I), float("nan"), dtype=torch.float32, device="cuda")
+    m.moe_grouped_gemm(cfg, m.MOE_STAGE_GATE_UP_RAW, R, m.to_device(offsets), m.to_device(ac[0]), m.to_device(asc[0]),
+                       m.make_weights(dev), out, ws)
+    assert m.moe_read_status(ws) == 0
+    want = np.stack([np.einsum("rk,rnk->rn", a[0], w[n][group]) for n in "13"], 1)
+    # multiples of 2^-6, magnitude below 2^18: exact in fp32 in any order
+    assert np.abs(want).max() < 2.0 ** 18 and np.array_equal(want * 64, np.rint(want * 64))
+    bad = np.argwhere(out[:R].cpu().numpy() != want)
+    assert bad.size == 0, f"{len(bad)} sums differ, first {bad[:4].tolist()}"
+    assert torch.isnan(out[R]).all()  # nothing behind the last row
+
+
+def test_mxfp4_gate_up_h(m):
+    """h leaves as MXFP4 of silu(gate) * up: equal to the quantised definition but where a value
+    sits on a border of the code grid, within fp32 noise, and there one code apart."""
+    import torch
+    cfg, dev, w, offsets, R, group, ws = _setup(m)
+    ac, asc, a = _matrices(4, 1, R, H, spread=0)
+    a, asc = a * 2.0 ** -8, asc - 8
+    out = torch.zeros((R, I // 2), dtype=torch.uint8, device="cuda")
+    osc = torch.zeros((R, I // 32), dtype=torch.uint8, device="cuda")
+    m.moe_grouped_gemm(cfg, m.MOE_STAGE_GATE_UP, R, m.to_device(offsets), m.to_device(ac[0]), m.to_device(asc[0]),
+                       m.make_weights(dev), out, ws, out_scale=osc)
+    assert m.moe_read_status(ws) == 0
+    g, u = (np.einsum("rk,rnk->rn", a[0], w[n][group]) for n in "13")
+    with np.errstate(over="ignore"):
+        c, s = ref.mx_quantize(g / (1 + np.exp(-g)) * u)
+    got, got_s = ref.unpack(out.cpu().numpy()).astype(int), osc.cpu().numpy().astype(int)
+    assert np.mean(got_s != s) < 1e-4 and np.abs(got_s - s).max() <= 1
+    same = np.repeat(got_s == s, 32, -1)
+    want = ref.unpack(c).astype(int)
+    assert np.mean(got[same] != want[same]) < 1e-4
+    assert np.abs((got & 7) - (want & 7))[same].max() <= 1
+
+
+def test_mxfp4_down_exact(m):
+    import torch
+    cfg, dev, w, offsets, R, group, ws = _setup(m)
+    ac, asc, a = _matrices(5, 1, R, I)
+    gate = np.random.default_rng(6).choice(np.array([0.5, 1.0, 2.0], np.float32), R)
+    y = torch.full((R + 1, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    for row_gate in (gate, None):
+        m.moe_grouped_gemm(cfg, m.MOE_STAGE_DOWN, R, m.to_device(offsets), m.to_device(ac[0]), m.to_device(asc[0]),
+                           m.make_weights(dev), y, ws, row_gate=None if row_gate is None else m.to_device(row_gate))
+        assert m.moe_read_status(ws) == 0
+        want = np.einsum("rk,rnk->rn", a[0], w["2"][group])
+        if row_gate is not None:
+            want = want * gate[:, None]
+        got = y.view(torch.int16).cpu().numpy().view(np.uint16)
+        bad = np.argwhere(got[:R] != synth.f32_to_bf16(want.astype(np.float32)))
+        assert bad.size == 0, f"{len(bad)} outputs differ, first {bad[:4].tolist()}"
+        assert (y[R] == 7.0).all()
+
+
+def mx_weights(m, seed, E, S, H, I, bias=False):
+    """Quantised normal weights on the device (by the library) and their values by matrix."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    wt = {"router_w": torch.empty((E, H), dtype=torch.bfloat16, device="cuda").normal_(0, H ** -0.5, generator=gen),
+          "router_bias": m.to_device(synth.zipf_bias(seed, E)) if bias else None}
+    for pre, n in (("", E), ("s", 1))[: 1 + S]:
+        for name, rows, cols in (("1", I, H), ("3", I, H), ("2", H, I)):
+            x = torch.empty((n, rows, cols), dtype=torch.bfloat16, device="cuda").normal_(0, cols ** -0.5, generator=gen)
+            c = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device="cuda")
+            s = torch.empty((n, rows, cols // 32), dtype=torch.uint8, device="cuda")
+            m.moe_quantize_fp4(m.MOE_WDTYPE_MXFP4, n, rows, cols, x, None, c, s)
+            wt[pre + "w" + name], wt[pre + "s" + name] = c, s
+    def of(pre):
+        return lambda e=0: [ref.mx_values(wt[pre + "w" + n][e].cpu().numpy(), wt[pre + "s" + n][e].cpu().numpy())
+                            for n in "132"]
+    return wt, of("") , of("s") if S else None
+
+
+# T, H, I, E, k, S, bias, sampled tokens
+LAYERS = [(40, 512, 512, 16, 2, 1, False, None), (300, 1024, 512, 24, 4, 1, True, 40), (77, 512, 1024, 12, 3, 0, False, None),
+          (1, 512, 512, 4, 4, 1, False, None), (1000, 512, 512, 3, 1, 0, True, 40), (64, 4096, 1536, 88, 8, 1, False, 10)]
+
+
+@pytest.mark.parametrize("T,H,I,E,k,S,bias,sample", LAYERS)
+def test_mxfp4_layer_parity(m, T, H, I, E, k, S, bias, sample):
+    """Quantise the weights, run the whole layer on them, and compare with the definition."""
+    import torch
+    wt, w, sh = mx_weights(m, 60 + T, E, S, H, I, bias)
+    x = synth.normal_bf16(61, 1, (T, H), 1.0)
+    rw = wt["router_w"].view(torch.int16).cpu().numpy().view(np.uint16)
+    rb = wt["router_bias"].cpu().numpy() if bias else None
+    idx_r, gate_r, logits_r = oracle.route(x, rw, rb, k, want_logits=True)
+    cfg = m.make_config(H, E, k, S, I, m.MOE_WDTYPE_MXFP4)
+    out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    gate = torch.empty((T, k), dtype=torch.float32, device="cuda")
+    ws = torch.empty(m.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    m.moe_forward(cfg, T, m.to_device(x), m.make_weights(wt), out, ws, topk_idx=idx, topk_w=gate)
+    assert m.moe_read_status(ws) == 0
+    check_routing(idx.cpu().numpy(), gate.cpu().numpy(), logits_r, idx_r, gate_r)
+    toks = np.flatnonzero(unique_tokens(logits_r, k))
+    if sample:
+        toks = np.sort(np.random.default_rng(T).choice(toks, sample, False))
+    want = ref.layer("mxfp4", synth.bf16_to_f32(x).astype(np.float64), idx_r, gate_r, w, sh, toks)
+    got = bf16_bits_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16)[toks])
+    err, per = frob_rel(got, want), rows_rel(got, want)
+    print(f"T={T}: rel Frobenius {err:.2e}, per-token max {per.max():.2e}")
+    assert err < 1e-2 and per.max() < 1e-2
