@@ -150,6 +150,25 @@ MOE_API int moe_forward(const moe_config* cfg, int64_t T, const void* x, const m
                 moe_stream_t stream);
 
 /*
+ * The whole layer forward for T <= MOE_FEW_MAX_TOKENS tokens in two kernels (the
+ * router, then everything else in one cooperative launch): the same layer and
+ * arguments as moe_forward, on every expert storage, for the calls where launches
+ * and GEMM prologues would cost more than the weights. h is rounded as in
+ * moe_forward (bf16, or the storage's quantisation); each token's expert outputs
+ * are gate-weighted and summed in fp32 without an intermediate rounding, the
+ * shared expert first, then its experts by ascending index: a token's result does
+ * not depend on the other tokens of the call. T * H must leave room for the
+ * weight ring in shared memory (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * H <=
+ * 65,536 always does. Needs a device that
+ * supports cooperative launches with the whole GPU free for them (no other
+ * kernel may hold its SMs forever). One workspace serves one call at a time.
+ */
+enum { MOE_FEW_MAX_TOKENS = 8 };
+MOE_API int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w, void* out,
+                            int32_t* topk_idx, float* topk_w, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
+
+/*
  * moe_forward from host memory: copies x_host [T, H] bf16 to the device,
  * runs the layer and copies the result into out_host [T, H] bf16; weights and
  * workspace are device memory. Synchronous: returns after out_host is written

@@ -12,7 +12,7 @@ The functions carry the names of the C entry points:
   moe_set_gemm_variant, moe_permute_noalloc, moe_rmsnorm, moe_combine_residual,
   moe_grouped_gemm, moe_read_status_detail, moe_debug_inject, moe_launch_count,
   moe_forward_ep_partial, moe_ep_reduce, moe_quantize_fp4, moe_fp4_global_scale,
-  moe_dequantize_fp4.
+  moe_dequantize_fp4, moe_forward_few.
 """
 from __future__ import annotations
 
@@ -36,6 +36,7 @@ MOE_ERR_MISALIGNED = 7
 MOE_GEMM_AUTO, MOE_GEMM_SINGLE, MOE_GEMM_PAIR, MOE_GEMM_SWAP = 0, 1, 2, 3
 MOE_STAGE_GATE_UP, MOE_STAGE_GATE_UP_RAW, MOE_STAGE_DOWN = 1, 2, 3
 MOE_INJECT_NONE, MOE_INJECT_GEMM_NO_LOADS = 0, 1
+MOE_FEW_MAX_TOKENS = 8
 
 _lib = None
 
@@ -72,6 +73,7 @@ def load():
     sig = {
         "moe_workspace_bytes": [cfgp, i64, ctypes.POINTER(sz)],
         "moe_forward": [cfgp, i64, vp, wp, vp, vp, vp, vp, sz, vp],
+        "moe_forward_few": [cfgp, i64, vp, wp, vp, vp, vp, vp, sz, vp],
         "moe_forward_host": [cfgp, i64, vp, wp, vp, vp, sz, vp],
         "moe_forward_host_async": [cfgp, i64, vp, wp, vp, vp, sz, vp],
         "moe_route": [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -156,6 +158,13 @@ def moe_forward(cfg, T, x, w: moe_weights, out, workspace, topk_idx=None, topk_w
     nb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     _check(load().moe_forward(ctypes.byref(cfg), T, _ptr(x), ctypes.byref(w), _ptr(out), _ptr(topk_idx),
                               _ptr(topk_w), _ptr(workspace), nb, _stream(stream)), "moe_forward")
+
+
+def moe_forward_few(cfg, T, x, w: moe_weights, out, workspace, topk_idx=None, topk_w=None, stream=None):
+    """moe_forward for T <= MOE_FEW_MAX_TOKENS tokens, in two kernels."""
+    nb = workspace.numel() * workspace.element_size()
+    _check(load().moe_forward_few(ctypes.byref(cfg), T, _ptr(x), ctypes.byref(w), _ptr(out), _ptr(topk_idx),
+                                  _ptr(topk_w), _ptr(workspace), nb, _stream(stream)), "moe_forward_few")
 
 
 def moe_forward_host(cfg, T, x_host, w: moe_weights, out_host, workspace, stream=None):

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "few.cuh"
 #include "moe.h"
 #include "ptx.cuh"
 
@@ -91,6 +92,19 @@ bool map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, ui
   cuuint32_t estr[2] = {1, 1};
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Weight rows of `bytes` bytes as [128 bytes, rows, lines of 128 bytes], boxes of 8
+// lines x box_rows rows, 128B swizzle (the few-token layer).
+bool map_rows(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_rows) {
+  cuuint64_t dims[3] = {128, rows, bytes / 128};
+  cuuint64_t strides[2] = {bytes, 128};
+  cuuint32_t box[3] = {128, box_rows, 8};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -696,6 +710,15 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   L.part = take(k2 > 1 ? (size_t)k2 * L.R * c.hidden * 4 : 0);
   L.x_stage = take((size_t)T * c.hidden * 2);
   L.out_stage = take((size_t)T * c.hidden * 2);
+  if (T > 0 && T <= MOE_FEW_MAX_TOKENS) {
+    // The few-token layer: list entries x 8 token slots of h.
+    const int64_t slots = (T * k + S) * MOE_FEW_MAX_TOKENS * c.inter;
+    const int block = fp8 ? 128 : mx ? 32 : 0;
+    L.few_counters = take((size_t)few_counters(c.wdtype, (int)T, k, S, c.inter) * 4);
+    L.few_h = take(block ? (size_t)slots * 4 : 0);
+    L.few_hq = take((size_t)slots * 2);
+    L.few_hs = take(block ? (size_t)(slots / block) * 4 : 0);
+  }
   L.total = off;
   return L;
 }
@@ -736,6 +759,65 @@ int moe_forward(const moe_config* cfg, int64_t T, const void* x, const moe_weigh
   if ((rc = run_permute(pp, s, prof)) != MOE_OK) return rc;
   if ((rc = run_experts(cfg, L, T, x, w, pp.pos, ws + L.y, ws, s, prof, (int64_t)cfg->top_k * T)) != MOE_OK) return rc;
   return run_combine(cfg, T, ws + L.y, pp.pos, out, s, prof);
+}
+
+int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w, void* out,
+                    int32_t* topk_idx, float* topk_w, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int rc = check_config(cfg, T);
+  if (rc != MOE_OK) return rc;
+  if (T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((rc = check_weights(cfg, w)) != MOE_OK) return rc;
+  if (!x || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(out, 16)) return MOE_ERR_MISALIGNED;
+  if ((topk_idx == nullptr) != (topk_w == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T && !few_fits(cfg->wdtype, (int)T, cfg->hidden)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  WsLayout L;
+  if ((rc = check_ws(cfg, T, workspace, workspace_bytes, &L)) != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  const int sms = sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  FewParams p{};
+  p.T = (int32_t)T;
+  p.H = cfg->hidden;
+  p.I = cfg->inter;
+  p.E = cfg->n_experts;
+  p.k = cfg->top_k;
+  p.S = cfg->n_shared;
+  p.n_counters = few_counters(cfg->wdtype, (int)T, cfg->top_k, cfg->n_shared, cfg->inter);
+  p.x = static_cast<const uint16_t*>(x);
+  p.router_w = static_cast<const uint16_t*>(w->router_w);
+  p.bias = w->router_bias;
+  p.w = *w;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.topk_idx = topk_idx;
+  p.topk_w = topk_w;
+  p.logits = reinterpret_cast<float*>(ws + L.logits_part);
+  p.h = reinterpret_cast<float*>(ws + L.few_h);
+  p.hq = reinterpret_cast<uint16_t*>(ws + L.few_hq);
+  p.hs = reinterpret_cast<float*>(ws + L.few_hs);
+  p.counters = reinterpret_cast<int*>(ws + L.few_counters);
+  p.status = reinterpret_cast<int*>(ws + L.status);
+  p.wait_ns = g_wait_ns;
+  p.inject = g_inject;
+  if (!get_encoder()) return MOE_ERR_CUDA;
+  FewMaps tm{};
+  const int per2 = cfg->wdtype == MOE_WDTYPE_BF16 ? 1 : cfg->wdtype == MOE_WDTYPE_FP8_E4M3 ? 2 : 4;
+  const int block = cfg->wdtype == MOE_WDTYPE_NVFP4 ? 16 : 32;
+  const uint64_t H = cfg->hidden, I = cfg->inter, E = cfg->n_experts;
+  auto one = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows, uint64_t K,
+                 uint32_t box_rows) {
+    return map_rows(code, cp, K * 2 / per2, rows, box_rows) &&
+           (per2 < 4 || map_u8(scale, sp, K / block, rows, 2048 / block, box_rows));
+  };
+  bool ok = one(&tm.w1, &tm.s1, w->w1, w->s1, E * I, H, 8) && one(&tm.w3, &tm.s3, w->w3, w->s3, E * I, H, 8) &&
+            one(&tm.w2, &tm.s2, w->w2, w->s2, E * H, I, 4);
+  if (cfg->n_shared)
+    ok = ok && one(&tm.sw1, &tm.ss1, w->sw1, w->ss1, I, H, 8) && one(&tm.sw3, &tm.ss3, w->sw3, w->ss3, I, H, 8) &&
+         one(&tm.sw2, &tm.ss2, w->sw2, w->ss2, H, I, 4);
+  if (!ok) return MOE_ERR_CUDA;
+  CUDA_TRY(launch_few(p, tm, cfg->wdtype, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return MOE_OK;
 }
 
 int moe_forward_host_async(const moe_config* cfg, int64_t T, const void* x_host, const moe_weights* w,

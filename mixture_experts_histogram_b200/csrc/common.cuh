@@ -28,7 +28,9 @@ __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_
 struct WsLayout {
   int64_t T, R, rows_pad, chunks, ksplit;
   size_t status, idx, gate, logits_part, chunk_base, counts, offsets, mt_prefix, mp_prefix;
-  size_t perm, pos, row_gate, xp, sxp, h, sh, y, part, x_stage, out_stage, total;
+  size_t perm, pos, row_gate, xp, sxp, h, sh, y, part, x_stage, out_stage;
+  size_t few_counters, few_h, few_hq, few_hs;  // T <= MOE_FEW_MAX_TOKENS only
+  size_t total;
 };
 
 WsLayout ws_layout(const moe_config& c, int64_t T, int num_sms);
