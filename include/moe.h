@@ -155,11 +155,11 @@ MOE_API int moe_forward(const moe_config* cfg, int64_t T, const void* x, const m
  * arguments as moe_forward, on every expert storage, for the calls where launches
  * and GEMM prologues would cost more than the weights. h is rounded as in
  * moe_forward (bf16, or the storage's quantisation); each token's expert outputs
- * are gate-weighted and summed in fp32 without an intermediate rounding, the
- * shared expert first, then its experts by ascending index: a token's result does
- * not depend on the other tokens of the call. T * H must leave room for the
- * weight ring in shared memory (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * H <=
- * 65,536 always does. Needs a device that
+ * are gate-weighted and summed in fp32 without an intermediate rounding, by
+ * ascending index and the shared expert last: a token's result does not depend on
+ * the other tokens of the call. The tokens' activations must leave room for the
+ * weight ring in shared memory (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * max(H, I)
+ * <= 65,536 always does. Needs a device that
  * supports cooperative launches with the whole GPU free for them (no other
  * kernel may hold its SMs forever). One workspace serves one call at a time.
  */

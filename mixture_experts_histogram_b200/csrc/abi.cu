@@ -96,12 +96,12 @@ bool map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, ui
   return r == CUDA_SUCCESS;
 }
 
-// Weight rows of `bytes` bytes as [128 bytes, rows, lines of 128 bytes], boxes of 8
-// lines x box_rows rows, 128B swizzle (the few-token layer).
-bool map_rows(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_rows) {
+// Weight rows of `bytes` bytes as [128 bytes, rows, lines of 128 bytes], boxes of
+// box_rows rows x box_lines lines, 128B swizzle (the few-token layer).
+bool map_rows(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_rows, uint32_t box_lines) {
   cuuint64_t dims[3] = {128, rows, bytes / 128};
   cuuint64_t strides[2] = {bytes, 128};
-  cuuint32_t box[3] = {128, box_rows, 8};
+  cuuint32_t box[3] = {128, box_rows, box_lines};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -712,12 +712,8 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   L.out_stage = take((size_t)T * c.hidden * 2);
   if (T > 0 && T <= MOE_FEW_MAX_TOKENS) {
     // The few-token layer: list entries x 8 token slots of h.
-    const int64_t slots = (T * k + S) * MOE_FEW_MAX_TOKENS * c.inter;
-    const int block = fp8 ? 128 : mx ? 32 : 0;
-    L.few_counters = take((size_t)few_counters(c.wdtype, (int)T, k, S, c.inter) * 4);
-    L.few_h = take(block ? (size_t)slots * 4 : 0);
-    L.few_hq = take((size_t)slots * 2);
-    L.few_hs = take(block ? (size_t)(slots / block) * 4 : 0);
+    L.few_counter = take(4);
+    L.few_h = take((size_t)(T * k + S) * MOE_FEW_MAX_TOKENS * c.inter * 4);
   }
   L.total = off;
   return L;
@@ -770,12 +766,13 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   if (!x || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(out, 16)) return MOE_ERR_MISALIGNED;
   if ((topk_idx == nullptr) != (topk_w == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (T && !few_fits(cfg->wdtype, (int)T, cfg->hidden)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T && !few_fits(cfg->wdtype, (int)T, cfg->hidden, cfg->inter, kRouterTargetCtas)) return MOE_ERR_UNSUPPORTED_SHAPE;
   WsLayout L;
   if ((rc = check_ws(cfg, T, workspace, workspace_bytes, &L)) != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
+  if (!few_fits(cfg->wdtype, (int)T, cfg->hidden, cfg->inter, sms)) return MOE_ERR_UNSUPPORTED_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   FewParams p{};
   p.T = (int32_t)T;
@@ -784,7 +781,6 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.E = cfg->n_experts;
   p.k = cfg->top_k;
   p.S = cfg->n_shared;
-  p.n_counters = few_counters(cfg->wdtype, (int)T, cfg->top_k, cfg->n_shared, cfg->inter);
   p.x = static_cast<const uint16_t*>(x);
   p.router_w = static_cast<const uint16_t*>(w->router_w);
   p.bias = w->router_bias;
@@ -794,9 +790,7 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.topk_w = topk_w;
   p.logits = reinterpret_cast<float*>(ws + L.logits_part);
   p.h = reinterpret_cast<float*>(ws + L.few_h);
-  p.hq = reinterpret_cast<uint16_t*>(ws + L.few_hq);
-  p.hs = reinterpret_cast<float*>(ws + L.few_hs);
-  p.counters = reinterpret_cast<int*>(ws + L.few_counters);
+  p.counter = reinterpret_cast<int*>(ws + L.few_counter);
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.wait_ns = g_wait_ns;
   p.inject = g_inject;
@@ -807,8 +801,9 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   const uint64_t H = cfg->hidden, I = cfg->inter, E = cfg->n_experts;
   auto one = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows, uint64_t K,
                  uint32_t box_rows) {
-    return map_rows(code, cp, K * 2 / per2, rows, box_rows) &&
-           (per2 < 4 || map_u8(scale, sp, K / block, rows, 2048 / block, box_rows));
+    const uint32_t lines = per2 < 4 ? 8 : 4;  // of a slab
+    return map_rows(code, cp, K * 2 / per2, rows, box_rows, lines) &&
+           (per2 < 4 || map_u8(scale, sp, K / block, rows, lines * 256 / block, box_rows));
   };
   bool ok = one(&tm.w1, &tm.s1, w->w1, w->s1, E * I, H, 8) && one(&tm.w3, &tm.s3, w->w3, w->s3, E * I, H, 8) &&
             one(&tm.w2, &tm.s2, w->w2, w->s2, E * H, I, 4);

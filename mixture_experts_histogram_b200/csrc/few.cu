@@ -13,19 +13,21 @@
 //            is 8 features: 8 rows of W1 and the same 8 rows of W3 make the 16 rows
 //            of an mma.sync tile whose 8 columns are the tokens, so a thread holds
 //            the gate and the up sum of the same feature.
-//   h        is stored in the form the down products read. FP8 and MXFP4 quantise
-//            it: whoever completes a 128- or 32-feature block does that.
 //   grid barrier, during which the rings fill with W2.
 //   down     each CTA owns H / CTAs output rows for every listed expert and adds
-//            the gate-weighted products in registers: no partial output leaves
-//            the SM, and the sum's order (experts ascending, the shared one first)
-//            does not depend on the other tokens.
+//            the gate-weighted products up: no partial output leaves the SM, and
+//            the sum's order (experts ascending, then the shared one) does not
+//            depend on the other tokens. Four warps bring each expert's h, as fp32
+//            from L2, into shared memory in the storage's activation format.
 //
-// One thread streams weight rows by TMA (1 KB of 16 rows a stage: boxes of 128 bytes
-// x 8 or 4 rows x 8 lines, 128B-swizzled; row by row bulk copies of 1 KB reached
-// 4.1 TB/s, boxes the HBM rate) into a ring; eight warps multiply, each taking every
-// eighth 64-byte chunk of the rows, and add up through shared memory once per tile. The shared expert's rows are
-// known before the routing is: their copies start before the logits are ready.
+// One thread streams weight rows by TMA (boxes of 128 bytes x 8 or 4 rows x 8 or 4
+// lines, 128B-swizzled; row by row bulk copies of 1 KB reached 4.1 TB/s, boxes the
+// HBM rate) into a ring, another the scale bytes of 4-bit storage; eight warps
+// multiply, each a whole stage in its turn, and two add up their partial sums in
+// stage order and finish the tiles. (With every stage split over the warps the waits
+// and the address arithmetic cost more than the products: 2.0 TB/s for FP8.) The
+// shared expert's rows are known before the routing is: their copies start before
+// the logits are ready.
 // Tensor-core work is mma.sync (m16n8): at 23 weight bytes per clock and SM the
 // MMAs are far from a limit, and 8 columns fit 8 tokens without padding.
 #include <cuda_bf16.h>
@@ -41,67 +43,80 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;                    // consumer warps
-constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;    // + the producer warp
+constexpr int kWarps = 8;                    // multiplying warps
+constexpr int kAcc = 2;                      // warps that add up
+constexpr int kPrep = 4;                     // warps that bring h
+constexpr int kConsumers = (kWarps + kAcc + kPrep) * 32;
+constexpr int kThreads = kConsumers + 64;    // + the two producer warps
+constexpr int kHRing = 16;                   // experts of h in shared memory at most (more than kWarps)
 constexpr int kRows = 16;                    // rows of a stage
-constexpr int kSlab = 1024;                  // bytes of a row in a stage
-constexpr int kChunk = 64;                   // bytes of a row that one warp takes at a time
-constexpr int kMaxRing = 16;
+constexpr int kLine = 128;                   // bytes of a row that a step multiplies
+constexpr int kMaxRing = 24;
 constexpr int kMaxU = kFewMaxTokens * kMaxTopK + 1;
 constexpr int kRouterThreads = 128;
 
-// Per storage: inputs per 2 bytes of a weight row, scale bytes per row and slab
-// (4-bit storage), padding of an activation row in shared memory that keeps the
-// fragment loads free of bank conflicts, and inputs per activation block (0:
-// activations stay bf16).
+// Per storage: inputs per 2 bytes of a weight row, bytes of a row in a stage (a
+// slab), scale bytes per row and slab (4-bit storage), padding of an activation row in shared memory that keeps the
+// fragment loads free of bank conflicts, and inputs per activation block that
+// has a scale (0: activations stay bf16).
 template <int kW>
 struct Fmt;
 template <>
 struct Fmt<MOE_WDTYPE_BF16> {
-  static constexpr int kPer2 = 1, kScaleSlab = 0, kXPad = 64, kBlock = 0;
+  static constexpr int kPer2 = 1, kSlab = 1024, kScaleSlab = 0, kXPad = 64, kBlock = 0;
 };
 template <>
 struct Fmt<MOE_WDTYPE_FP8_E4M3> {
-  static constexpr int kPer2 = 2, kScaleSlab = 0, kXPad = 16, kBlock = 128;
+  static constexpr int kPer2 = 2, kSlab = 1024, kScaleSlab = 0, kXPad = 16, kBlock = 128;
 };
 template <>
 struct Fmt<MOE_WDTYPE_NVFP4> {
-  static constexpr int kPer2 = 4, kScaleSlab = kSlab / 8, kXPad = 64, kBlock = 0;
+  static constexpr int kPer2 = 4, kSlab = 512, kScaleSlab = kSlab / 8, kXPad = 64, kBlock = 128;
 };
 template <>
 struct Fmt<MOE_WDTYPE_MXFP4> {
-  static constexpr int kPer2 = 4, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 32;
+  static constexpr int kPer2 = 4, kSlab = 512, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 32;
 };
 
 template <int kW>
 struct Smem {
   using F = Fmt<kW>;
-  // A stage's scales: 16 rows of scale bytes, or 8 + 8 fp32 block scales.
-  static constexpr int kStageScales = kW == MOE_WDTYPE_FP8_E4M3 ? 128 : kRows * F::kScaleSlab;
-  static constexpr int kStage = kRows * kSlab + kStageScales;
-  // Fixed part: barriers, tables, reduction buffers. Then x, the scales, the tiles.
+  static constexpr int kStageScales = kRows * F::kScaleSlab;  // a stage's scale bytes
+  static constexpr int kStage = kRows * F::kSlab + kStageScales;
+  // Fixed part: barriers, tables, partial sums. Then the activations (x, later rows
+  // of h), the scale bytes and the weight tiles.
   static constexpr int kBars = 0;
-  static constexpr int kMisc = kBars + 2 * kMaxRing * 8;             // abort flag, list length
+  static constexpr int kNumBars = 2 * kMaxRing + 2 * kWarps + 2 * kHRing + 2 + kAcc;
+  static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;  // abort flag, list length
   static constexpr int kTopIdx = kMisc + 64;                         // int [8][16]
   static constexpr int kTopW = kTopIdx + kFewMaxTokens * kMaxTopK * 4;
   static constexpr int kBits = kTopW + kFewMaxTokens * kMaxTopK * 4; // uint [16] chosen experts, int [16] prefix
   static constexpr int kList = kBits + 2 * 16 * 4;                   // int [kMaxU] experts
   static constexpr int kUsed = kList + ((kMaxU * 4 + 15) / 16) * 16; // uint [kMaxU] token masks
-  static constexpr int kGate = kUsed + ((kMaxU * 4 + 15) / 16) * 16; // float [kMaxU][8]
-  static constexpr int kRed = kGate + kMaxU * kFewMaxTokens * 4;     // float [2][kWarps][4][32]
-  static constexpr int kX = kRed + 2 * kWarps * 128 * 4;             // activations
+  static constexpr int kFirst = kUsed + ((kMaxU * 4 + 15) / 16) * 16;  // int [kMaxU + 1] rows of h before an entry
+  static constexpr int kGate = kFirst + ((kMaxU * 4 + 4 + 15) / 16) * 16;  // float [kMaxU][8]
+  static constexpr int kRed = kGate + kMaxU * kFewMaxTokens * 4;     // float [kWarps][32][4] partial sums
+  static constexpr int kDown = kRed + kWarps * 128 * 4;              // float [kFewDownTiles][32][4] output sums
+  static constexpr int kX = kDown + kFewDownTiles * 128 * 4;
   static_assert(kX % 16 == 0, "alignment");
-  static __host__ __device__ int x_pitch(int H) { return H * 2 + F::kXPad; }
-  static __host__ __device__ int x_scales(int H) { return F::kBlock ? H / F::kBlock : 0; }
-  static __host__ __device__ int scale_offset(int T, int H) {
-    return (kX + T * x_pitch(H) + T * x_scales(H) * 4 + 127) / 128 * 128;
+  // A row of K activations: operands, padding, block scales.
+  static __host__ __device__ int scales_at(int K) { return K * 2 + F::kXPad; }
+  static __host__ __device__ int pitch(int K) {
+    return F::kBlock ? (scales_at(K) + K / F::kBlock * 4 + 63) / 128 * 128 + 64 + (F::kXPad == 16 ? 16 : 0) : scales_at(K);
   }
-  static __host__ __device__ int tile_offset(int T, int H, int stages) {
-    return (scale_offset(T, H) + stages * kStageScales + 1023) / 1024 * 1024;
+  // Bytes for T rows of x, then as many rows of h as fit, T at least.
+  static __host__ __device__ int act_bytes(int T, int H, int I) {
+    const int x = T * pitch(H), h = T * pitch(I);
+    return x > h ? x : h;
   }
-  static __host__ __device__ int stages(int T, int H) {
-    const int n = (kFewSmem - 2048 - scale_offset(T, H)) / kStage;  // both alignments
+  static __host__ __device__ int scale_offset(int T, int H, int I) {
+    return (kX + act_bytes(T, H, I) + 127) / 128 * 128;
+  }
+  static __host__ __device__ int tile_offset(int T, int H, int I, int stages) {
+    return (scale_offset(T, H, I) + stages * kStageScales + 1023) / 1024 * 1024;
+  }
+  static __host__ __device__ int stages(int T, int H, int I) {
+    const int n = (kFewSmem - 2048 - scale_offset(T, H, I)) / kStage;  // both alignments
     return n > kMaxRing ? kMaxRing : n;
   }
 };
@@ -109,15 +124,14 @@ struct Smem {
 // ------------------------------------------------------------------ router --
 
 // One CTA per expert: logits [T, E] of all tokens, fp32 sums in a fixed order.
-// CTA 0 also clears the status record and the counters of the second kernel.
+// CTA 0 also clears the status record and the second kernel's barrier counter.
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewParams p) {
   pdl_wait();
   pdl_trigger();  // after the wait: the next kernel may read everything that this one may
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < (int)(kStatusBytes / 4); i += kRouterThreads) p.status[i] = 0;
+    if (threadIdx.x == 0) *p.counter = 0;
   }
-  const int n_count = p.n_counters;
-  for (int i = blockIdx.x * kRouterThreads + threadIdx.x; i < n_count; i += gridDim.x * kRouterThreads) p.counters[i] = 0;
   __shared__ float part[kRouterThreads / 32][kFewMaxTokens];
   const int e = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (int64_t)e * (p.H / 8);
@@ -187,18 +201,25 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Activations are 16-bit operands: bf16 (BF16, NVFP4), or the f16 values of the
-// E4M3 and E2M1 codes (exact). Element k of a row sits in place, but for NVFP4:
-// within 128 inputs, [word j][lane c][pair r] holds inputs 32 c + 8 j + r and
-// + r + 4, the pairs that its expansion of a code word gives.
+// Activations are 16-bit operands: bf16 (BF16); the f16 values of the E4M3 and E2M1
+// codes (FP8, MXFP4; exact); or, for NVFP4, whose activations are not quantised, f16
+// next to a power of two for each 128 inputs that puts the largest at [2^14, 2^15):
+// what f16 cannot hold then is below 2^-39 of that largest one, where the fp32 sums
+// have 24 bits. Values lie in input order, but for NVFP4, whose groups of 8 inputs
+// are transposed 4 x 4 within 32 x 4 inputs, as its lanes read them.
 template <int kW>
-__device__ __forceinline__ int x_place(int k) {
-  if constexpr (kW == MOE_WDTYPE_NVFP4) {
-    const int c = (k >> 5) & 3, j = (k >> 3) & 3, i = k & 7;
-    return (k & ~127) + 32 * j + 8 * c + 2 * (i & 3) + (i >> 2);
-  } else {
-    return k;
-  }
+__device__ __forceinline__ int x_group(int v) {
+  return kW == MOE_WDTYPE_NVFP4 ? (v & ~15) | (v & 3) << 2 | ((v >> 2) & 3) : v;
+}
+
+// The f16 values of four E4M3 codes, in order.
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two) {
@@ -219,115 +240,198 @@ __device__ __forceinline__ void f16_of_e2m1x8(uint32_t w, uint32_t (&v)[4]) {
       : "r"(w));
 }
 
-// E8M0 byte as fp32 (0: 2^-127; 255: infinity, which makes the sums non-finite).
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Byte i of a word of E8M0 scales as fp32 (0: 2^-127; 255: infinity, which makes the
+// sums non-finite).
 __device__ __forceinline__ float e8m0_weight(uint32_t word, int i) {
   return __uint_as_float(max((word << (24 - 8 * i)) >> 24 << 23, 0x00400000u));
 }
 
-// A lane's activation fragment of one chunk: the token's 16 (BF16), 32 (FP8) or
-// 64 (4-bit) bytes, and its block scales for tokens 2c and 2c + 1.
-template <int kW>
-struct XFrag {
-  static constexpr int kVecs = kW == MOE_WDTYPE_BF16 ? 1 : kW == MOE_WDTYPE_FP8_E4M3 ? 2 : 4;
-  static constexpr int kScales = kW == MOE_WDTYPE_MXFP4 ? 4 : 1;
-  uint4 v[kVecs];
-  float s0[kScales], s1[kScales];
-};
-
-// Byte offset of vector i of lane c's fragment of chunk q in a row of activations.
-template <int kW>
-__device__ __forceinline__ int frag_offset(int q, int c, int i) {
-  if constexpr (kW == MOE_WDTYPE_BF16) return q * 64 + 16 * c;
-  if constexpr (kW == MOE_WDTYPE_FP8_E4M3) return q * 128 + 32 * c + 16 * i;
-  return q * 256 + 64 * i + 16 * c;
-}
-
-// Where a lane's two weight rows (g and g + 8 of the tile) lie in a stage: line l
-// at base + l * step, 16-byte unit i of it at ((i ^ x) << 4) for x = (l * step +
-// base) / 128 % 8 (the 128-byte swizzle).
-struct Rows {
-  const uint8_t* tile;     // the stage
-  const uint8_t* scales;   // of the stage
-  int r0, r1, step;        // offsets of line 0 of the two rows, and from line to line
-  __device__ __forceinline__ const uint8_t* at(int row, int line, int unit) const {
-    const int o = row + line * step;
-    return tile + o + ((unit ^ ((o >> 7) & 7)) << 4);
+// Sums of a stage, in as many independent chains of MMAs as hide their latency.
+struct Sums {
+  float a[4][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[i][j] = 0.0f;
+  }
+  __device__ __forceinline__ float4 total() const {
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = (a[0][j] + a[1][j]) + (a[2][j] + a[3][j]);
+    return make_float4(s[0], s[1], s[2], s[3]);
   }
 };
 
-// acc += rows x tokens over one chunk (64 bytes of the stage's 16 rows). FP8:
-// sb0, sb1 = weight scales of rows 0..7 and 8..15.
+// acc += d * s * w: rows g (w0) and g + 8 (w1) of the columns with scales s.
+__device__ __forceinline__ void weigh(float (&acc)[4], const float (&d)[4], float2 s, float w0, float w1) {
+  const float2 z = make_float2(0.0f, 0.0f);
+  const float2 a = fma2(fma2(make_float2(d[0], d[1]), s, z), make_float2(w0, w0), make_float2(acc[0], acc[1]));
+  const float2 b = fma2(fma2(make_float2(d[2], d[3]), s, z), make_float2(w1, w1), make_float2(acc[2], acc[3]));
+  acc[0] = a.x;
+  acc[1] = a.y;
+  acc[2] = b.x;
+  acc[3] = b.y;
+}
+
+// What a lane needs of a stage: the weight tile and its scale bytes, the offsets of
+// line 0 of its two rows (g, g + 8) and from line to line, the token's activations
+// (token g) and the block scales of the tokens of its columns (2c, 2c + 1).
+struct Operands {
+  const uint8_t *tile, *scales, *x;
+  const float *s0, *s1;
+  int r0, r1, step;
+};
+
+// acc += rows x tokens over line l of the stage, whose number in the whole row is kl.
+// sb0, sb1 (FP8): weight scales of rows g and g + 8 in this line's 128 inputs.
 template <int kW>
-__device__ __forceinline__ void chunk_mma(float (&acc)[4], const Rows& rows, int q, const XFrag<kW>& x, float sb0,
-                                          float sb1, int lane) {
+__device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, int kl, float sb0, float sb1, int lane) {
   using F = Fmt<kW>;
   const int g = lane / 4, c = lane % 4;
-  const int line = q / 2, unit = (q & 1) * 4;
+  const int o0 = o.r0 + l * o.step, o1 = o.r1 + l * o.step;
+  // The 128-byte swizzle: 16-byte unit i of a line lies at i ^ (line address / 128 % 8).
+  const int x0 = (o0 >> 7 & 7) << 4, x1 = (o1 >> 7 & 7) << 4;
   if constexpr (kW == MOE_WDTYPE_MXFP4) {
-    // Two MMAs per 32-input block (lane c takes the block's word c); the block's
-    // sum is weighted by both scales.
-    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(rows.scales + g * F::kScaleSlab + q * 4);
-    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(rows.scales + (g + 8) * F::kScaleSlab + q * 4);
+    // Eight 32-input blocks, two MMAs each (lane c takes the block's word c); a
+    // block's sum is weighted by both scales.
+    const uint8_t *a0 = o.tile + o0 + 4 * c, *a1 = o.tile + o1 + 4 * c;
+    const uint2 w0 = *reinterpret_cast<const uint2*>(o.scales + g * F::kScaleSlab + l * 8);
+    const uint2 w1 = *reinterpret_cast<const uint2*>(o.scales + (g + 8) * F::kScaleSlab + l * 8);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      uint32_t va[4], vb[4];
-      f16_of_e2m1x8(reinterpret_cast<const uint32_t*>(rows.at(rows.r0, line, unit + b))[c], va);
-      f16_of_e2m1x8(reinterpret_cast<const uint32_t*>(rows.at(rows.r1, line, unit + b))[c], vb);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(d, va[0], vb[0], va[1], vb[1], x.v[b].x, x.v[b].y);
-      mma_f16(d, va[2], vb[2], va[3], vb[3], x.v[b].z, x.v[b].w);
-      const float f0 = e8m0_weight(w0, b), f1 = e8m0_weight(w1, b);
-      acc[0] = fmaf(d[0] * x.s0[b], f0, acc[0]);
-      acc[1] = fmaf(d[1] * x.s1[b], f0, acc[1]);
-      acc[2] = fmaf(d[2] * x.s0[b], f1, acc[2]);
-      acc[3] = fmaf(d[3] * x.s1[b], f1, acc[3]);
-    }
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(rows.at(rows.r0, line, unit + c));
-    const uint4 b = *reinterpret_cast<const uint4*>(rows.at(rows.r1, line, unit + c));
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-    if constexpr (kW == MOE_WDTYPE_BF16) {
-      mma_b16(acc, a.x, b.x, a.y, b.y, x.v[0].x, x.v[0].y);
-      mma_b16(acc, a.z, b.z, a.w, b.w, x.v[0].z, x.v[0].w);
-    } else if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-      const uint32_t xv[8] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w, x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < 2; ++h) {
+      const float4 s0 = reinterpret_cast<const float4*>(o.s0)[2 * kl + h];
+      const float4 s1 = reinterpret_cast<const float4*>(o.s1)[2 * kl + h];
+      const float sx0[4] = {s0.x, s0.y, s0.z, s0.w}, sx1[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        mma_f16(d, f16x2_of_e4m3x2(aw[j]), f16x2_of_e4m3x2(bw[j]), f16x2_of_e4m3x2(aw[j] >> 16),
-                f16x2_of_e4m3x2(bw[j] >> 16), xv[2 * j], xv[2 * j + 1]);
-      acc[0] = fmaf(d[0], x.s0[0] * sb0, acc[0]);
-      acc[1] = fmaf(d[1], x.s1[0] * sb0, acc[1]);
-      acc[2] = fmaf(d[2], x.s0[0] * sb1, acc[2]);
-      acc[3] = fmaf(d[3], x.s1[0] * sb1, acc[3]);
-    } else {
-      // Codes times block scale as bf16, exactly: the code's bits placed in the
-      // bf16 exponent and mantissa are code x 2^-126, the scale comes as s x 2^118.
-      auto scales = [](const uint8_t* at, uint32_t (&s)[2]) {
-        const uint32_t h2 = f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(at));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        s[0] = pack_bf16x2(f.x * 0x1p118f, f.x * 0x1p118f);
-        s[1] = pack_bf16x2(f.y * 0x1p118f, f.y * 0x1p118f);
-      };
-      uint32_t s0[2], s1[2];
-      scales(rows.scales + g * F::kScaleSlab + q * 8 + 2 * c, s0);
-      scales(rows.scales + (g + 8) * F::kScaleSlab + q * 8 + 2 * c, s1);
-      auto expand = [](uint32_t w, int r, uint32_t s) {
-        const uint32_t t = w << (12 - 4 * r);
-        const uint32_t v = (t & 0x80008000u) | ((t >> 6) & 0x01c001c0u);
-        uint32_t o;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(v), "r"(s));
-        return o;
-      };
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t sa = s0[j / 2], sb = s1[j / 2];
-        mma_b16(acc, expand(aw[j], 0, sa), expand(bw[j], 0, sb), expand(aw[j], 1, sa), expand(bw[j], 1, sb), x.v[j].x,
-                x.v[j].y);
-        mma_b16(acc, expand(aw[j], 2, sa), expand(bw[j], 2, sb), expand(aw[j], 3, sa), expand(bw[j], 3, sb), x.v[j].z,
-                x.v[j].w);
+      for (int b = 0; b < 4; ++b) {
+        const int u = (4 * h + b) << 4;
+        uint32_t va[4], vb[4];
+        f16_of_e2m1x8(*reinterpret_cast<const uint32_t*>(a0 + (u ^ x0)), va);
+        f16_of_e2m1x8(*reinterpret_cast<const uint32_t*>(a1 + (u ^ x1)), vb);
+        const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 512 + (4 * h + b) * 64 + 16 * c);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(d, va[0], vb[0], va[1], vb[1], x.x, x.y);
+        mma_f16(d, va[2], vb[2], va[3], vb[3], x.z, x.w);
+        weigh(acc.a[b], d, make_float2(sx0[b], sx1[b]), e8m0_weight(h ? w0.y : w0.x, b),
+              e8m0_weight(h ? w1.y : w1.x, b));
       }
     }
+  } else {
+    const uint8_t *a0 = o.tile + o0 + ((c << 4) ^ x0), *a1 = o.tile + o1 + ((c << 4) ^ x1);
+    float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // halves of the line, 64 bytes
+      const uint32_t flip = h ? 64u : 0u;
+      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(a0) ^ flip);
+      const uint4 b = *reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(a1) ^ flip);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      if constexpr (kW == MOE_WDTYPE_BF16) {
+        const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 128 + h * 64 + 16 * c);
+        mma_b16(acc.a[2 * h], aw[0], bw[0], aw[1], bw[1], x.x, x.y);
+        mma_b16(acc.a[2 * h + 1], aw[2], bw[2], aw[3], bw[3], x.z, x.w);
+      } else if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+        const uint4* xp = reinterpret_cast<const uint4*>(o.x + kl * 256 + h * 128 + 32 * c);
+        const uint4 xa = xp[0], xb = xp[1];
+        const uint32_t xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a_lo, a_hi, b_lo, b_hi;
+          f16_of_e4m3x4(aw[j], a_lo, a_hi);
+          f16_of_e4m3x4(bw[j], b_lo, b_hi);
+          mma_f16(d[j & 1], a_lo, b_lo, a_hi, b_hi, xv[2 * j], xv[2 * j + 1]);
+        }
+      } else {
+        // NVFP4: the codes times their 16-input scale, exact in f16 (5 significant
+        // bits, 2^-10 to 2688); 128 inputs a half, with one activation scale.
+        const uint32_t sa = *reinterpret_cast<const uint16_t*>(o.scales + g * F::kScaleSlab + l * 16 + h * 8 + 2 * c);
+        const uint32_t sb = *reinterpret_cast<const uint16_t*>(o.scales + (g + 8) * F::kScaleSlab + l * 16 + h * 8 + 2 * c);
+        const uint32_t wa[2] = {f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x11))};
+        const uint32_t wb[2] = {f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x11))};
+        float e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 512 + h * 256 + 64 * j + 16 * c);
+          uint32_t va[4], vb[4];
+          f16_of_e2m1x8(aw[j], va);
+          f16_of_e2m1x8(bw[j], vb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            va[i] = mul_f16x2(va[i], wa[j / 2]);
+            vb[i] = mul_f16x2(vb[i], wb[j / 2]);
+          }
+          mma_f16(e[j & 1], va[0], vb[0], va[1], vb[1], x.x, x.y);
+          mma_f16(e[j & 1], va[2], vb[2], va[3], vb[3], x.z, x.w);
+        }
+        const float2 sx = make_float2(o.s0[2 * kl + h], o.s1[2 * kl + h]);
+        weigh(acc.a[0], e[0], sx, 1.0f, 1.0f);
+        weigh(acc.a[1], e[1], sx, 1.0f, 1.0f);
+      }
+    }
+    if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[0][i] += d[1][i];
+      weigh(acc.a[0], d[0], make_float2(o.s0[kl], o.s1[kl]), sb0, sb1);
+    }
+  }
+}
+
+// 8 values of a row (inputs 8 v .. 8 v + 7; all lanes of the warp take part, `live`
+// ones hold values) into the operand row at `row` with scales behind it. FP8:
+// kDivide quantises by IEEE quotients (x), else by the scale's reciprocal (h).
+template <int kW, bool kDivide>
+__device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v, const float (&f)[8], bool live) {
+  using F = Fmt<kW>;
+  if constexpr (F::kBlock == 0) {
+    if (live)
+      *reinterpret_cast<uint4*>(row + v * 16) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  } else {
+    uint32_t m = amax_bits<8>(f);
+    constexpr int kLanes = F::kBlock / 8;  // 16 (FP8, NVFP4) or 4 (MXFP4) lanes share a block
+#pragma unroll
+    for (int o = 1; o < kLanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!live) return;
+    float s;
+    uint32_t h[4];
+    if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+      // (A NaN fails the comparison, keeps scale 1 and becomes a NaN code.)
+      const float amax = __uint_as_float(m);
+      s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      const float r = kDivide ? 1.0f : __frcp_rn(s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 q = kDivide ? make_float2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s))
+                                 : make_float2(f[2 * j] * r, f[2 * j + 1] * r);
+        h[j] = f16x2_of_e4m3x2(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
+      }
+    } else if constexpr (kW == MOE_WDTYPE_MXFP4) {
+      const uint32_t sb = e8m0_of(m);
+      f16_of_e2m1x8(sb == 255u ? 0u : e2m1x8(f, e8m0_rcp(sb)), h);
+      s = e8m0_value(sb);
+    } else {
+      // bf16 values (h is rounded to bf16, as x is) times 2^k, k = 14 - floor(log2(m)); a
+      // non-finite or zero block keeps k = 0. 2^k and 2^-k are both normal for eb in [15, 254].
+      const uint32_t eb = max(m >> 23, 15u);
+      const bool plain = m == 0u || eb == 255u;
+      const float r = plain ? 1.0f : __uint_as_float((268u - eb) << 23);
+      s = plain ? 1.0f : __uint_as_float((eb - 14u) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b2 = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+        const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&b2));
+        const __half2 v2 = __floats2half2_rn(q.x * r, q.y * r);
+        h[j] = *reinterpret_cast<const uint32_t*>(&v2);
+      }
+    }
+    *reinterpret_cast<uint4*>(row + x_group<kW>(v) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (v % kLanes == 0) reinterpret_cast<float*>(row + scales_at)[v / kLanes] = s;
   }
 }
 
@@ -359,24 +463,23 @@ __device__ __forceinline__ GateUpWalk gate_up_walk(const FewParams& p, int u0, i
                     u0, per};
 }
 
-// Down: output rows [r, end), multiples of 4, up to 16 at a time within a 128-row
-// block, every list entry each.
-struct DownWalk {
-  int r, end;
-  __device__ __forceinline__ bool next(int& r0, int& n) {
-    if (r >= end) return false;
-    r0 = r;
-    n = min(min(16, end - r), 128 - r % 128);
-    r += n;
-    return true;
-  }
+// Down: this CTA's output rows, a multiple of 4 of them, in tiles of up to 16; every
+// list entry in turn (the shared expert last), every tile of it.
+struct DownRows {
+  int r0, rows, tiles;
+  __device__ __forceinline__ int first(int tile) const { return r0 + 16 * tile; }
+  __device__ __forceinline__ int count(int tile) const { return min(16, rows - 16 * tile); }
 };
 
-__device__ __forceinline__ DownWalk down_walk(const FewParams& p) {
+__device__ __forceinline__ DownRows down_rows(const FewParams& p) {
   const int units = p.H / 4;
-  return DownWalk{4 * (int)((int64_t)units * blockIdx.x / gridDim.x),
-                  4 * (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x)};
+  const int a = 4 * (int)((int64_t)units * blockIdx.x / gridDim.x);
+  const int b = 4 * (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  return DownRows{a, b - a, (b - a + 15) / 16};
 }
+
+// List entry of step i of the down phase.
+__device__ __forceinline__ int down_entry(int i, int U, int S) { return S == 0 ? i : i + 1 < U ? i + 1 : 0; }
 
 struct Ring {
   int stage = 0;
@@ -389,51 +492,111 @@ struct Ring {
   }
 };
 
-// Copies the K slabs of a tile of `boxes` boxes of `box_rows` rows each, box b from
-// row(b) of map(b); 4-bit storage: their scales from smap(b). FP8: lanes 0..15
-// fetch the weight scales of the slab's K blocks from fs0 (rows 0..7) and fs1.
-template <int kW, typename Map, typename SMap, typename Row>
-__device__ __forceinline__ bool load_tile(const FewParams& p, uint8_t* tiles, uint8_t* scales, uint64_t* full,
-                                          uint64_t* empty, Ring& rg, int boxes, int box_rows, Map map, SMap smap, Row row,
-                                          const float* fs0, const float* fs1, int row_bytes, int lane,
-                                          volatile int* abort_flag, uint32_t& issued, uint32_t& issued_phase) {
+// A producer thread's view of the ring: kScales false: the weight rows, true: their scale bytes.
+template <bool kScales>
+struct Producer {
+  uint8_t* dst;
+  uint64_t *full, *empty;
+  int n_stages;
+  Ring rg;
+  uint32_t issued = 0, issued_phase = 0;  // per slot: loaded at all, and the phase of the last load
+};
+
+// Loads the K slabs of a tile: `boxes` boxes of kBoxRows rows from row0 (with two
+// maps, the same rows of each: gate and up). One thread, and as few instructions per
+// stage as possible: at the HBM rate a stage takes about 700 clocks, and a TMA
+// instruction costs its thread more than 100.
+template <int kW, bool kScales, int kBoxRows, bool kTwoMaps>
+__device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>& pr, int boxes, const CUtensorMap* m0,
+                                          const CUtensorMap* m1, int row0, int slabs, volatile int* abort_flag) {
   using F = Fmt<kW>;
-  using L = Smem<kW>;
-  for (int k0 = 0; k0 < row_bytes; k0 += kSlab) {
-    if (!warp_wait<false>(&empty[rg.stage], rg.phase ^ 1u, p.status, abort_flag, 0x2001, k0, p.wait_ns)) return false;
-    uint8_t* st = tiles + rg.stage * (kRows * kSlab);
-    uint8_t* sc = scales + rg.stage * L::kStageScales;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&full[rg.stage], (uint32_t)(boxes * box_rows * (kSlab + F::kScaleSlab)));
-      for (int b = 0; b < boxes; ++b) {
-        tma_load_rows(st + b * box_rows * kSlab, map(b), &full[rg.stage], row(b), k0 / 128);
-        if (F::kScaleSlab)
-          tma_load_2d(sc + b * box_rows * F::kScaleSlab, smap(b), &full[rg.stage], k0 / kSlab * F::kScaleSlab, row(b));
-      }
+  constexpr int kBytes = kScales ? F::kScaleSlab : F::kSlab;  // of a row
+  const uint32_t bytes = (uint32_t)(boxes * kBoxRows * kBytes);
+  for (int k = 0; k < slabs; ++k) {
+    const int st = pr.rg.stage;
+    if (!mbar_wait(&pr.empty[st], pr.rg.phase ^ 1u, p.status, abort_flag, 0x2001, k, p.wait_ns)) return false;
+    uint64_t* bar = &pr.full[st];
+    mbar_arrive_expect_tx(bar, bytes);
+    uint8_t* dst = pr.dst + st * (kRows * kBytes);
+    auto load = [&](uint8_t* to, const CUtensorMap* m, int row) {
+      if constexpr (kScales) tma_load_2d(to, m, bar, k * kBytes, row);
+      else tma_load_rows(to, m, bar, row, k * (kBytes / 128));
+    };
+    if constexpr (kTwoMaps) {
+      load(dst, m0, row0);
+      load(dst + kBoxRows * kBytes, m1, row0);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kRows / kBoxRows; ++b)
+        if (b < boxes) load(dst + b * kBoxRows * kBytes, m0, row0 + b * kBoxRows);
     }
-    if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-      // K block k0 / 128 + lane % 8 of rows 0..7 (lanes 0..7) or 8..15 (lanes 8..15).
-      if (lane < 16 && k0 + lane % 8 * 128 < row_bytes)
-        cp_async_4(sc + lane * 4, (lane < 8 ? fs0 : fs1) + k0 / 128 + lane % 8);
-      cp_async_arrive(&full[rg.stage]);
-    }
-    issued |= 1u << rg.stage;
-    issued_phase = (issued_phase & ~(1u << rg.stage)) | (rg.phase << rg.stage);
-    rg.step(p.n_stages);
+    pr.issued |= 1u << st;
+    pr.issued_phase ^= ((pr.issued_phase >> st ^ pr.rg.phase) & 1u) << st;
+    pr.rg.step(pr.n_stages);
   }
   return true;
+}
+
+// Everything a producer warp does (lane 0 loads).
+template <int kW, bool kScales>
+__device__ __forceinline__ void produce(const FewParams& p, const FewMaps& tm, uint8_t* dst, uint64_t* full,
+                                        uint64_t* empty, const int* list, volatile int* n_list, volatile int* abort_flag,
+                                        int h_slabs, int i_slabs, int lane) {
+  Producer<kScales> pr{dst, full, empty, p.n_stages};
+  bool ok = p.inject != 1;
+  const CUtensorMap *g = kScales ? &tm.s1 : &tm.w1, *u = kScales ? &tm.s3 : &tm.w3, *d = kScales ? &tm.s2 : &tm.w2;
+  const CUtensorMap *sg = kScales ? &tm.ss1 : &tm.sw1, *su = kScales ? &tm.ss3 : &tm.sw3,
+                    *sd = kScales ? &tm.ss2 : &tm.sw2;
+  auto gate_up = [&](GateUpWalk w) {
+    Tile t;
+    while (ok && w.next(t)) {
+      const bool sh = p.S && t.u == 0;
+      ok = load_tile<kW, kScales, 8, true>(p, pr, 2, sh ? sg : g, sh ? su : u, (sh ? 0 : list[t.u]) * p.I + t.r0, h_slabs,
+                                           abort_flag);
+    }
+  };
+  if (lane == 0) gate_up(gate_up_walk(p, 0, p.S));  // the shared expert: needs no routing
+  __syncwarp();
+  named_bar_sync(1, kThreads);  // the expert list is ready
+  if (lane != 0) return;
+  const int U = *n_list;
+  gate_up(gate_up_walk(p, p.S, U - p.S));
+  const DownRows dr = down_rows(p);
+  for (int i = 0; i < U && ok; ++i) {
+    const int e = down_entry(i, U, p.S);
+    const bool sh = p.S && e == 0;
+    const int base = (sh ? 0 : list[e]) * p.H;
+    for (int tile = 0; tile < dr.tiles && ok; ++tile)
+      ok = load_tile<kW, kScales, 4, false>(p, pr, dr.count(tile) / 4, sh ? sd : d, nullptr, base + dr.first(tile),
+                                            i_slabs, abort_flag);
+  }
+  // Let every copy land before the thread leaves (the others wait for them too, unless a wait gave up).
+  for (int s = 0; s < p.n_stages; ++s) {
+    if (!(pr.issued & (1u << s))) continue;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&full[s], (pr.issued_phase >> s) & 1u) && global_timer_ns() - t0 < 200000000ull) {}
+  }
 }
 
 // ---------------------------------------------------------------- the layer --
 
 template <int kW>
-__global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParams p, const __grid_constant__ FewMaps tm) {
+__global__ void __launch_bounds__(kThreads, 1)
+    few_experts_kernel(const FewParams p, const __grid_constant__ FewMaps tm) {
   using F = Fmt<kW>;
   using L = Smem<kW>;
+  constexpr bool kScaleBytes = F::kScaleSlab != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + kMaxRing;
+  uint64_t* pfull = empty + kMaxRing;    // a warp's partial sums are in its buffer
+  uint64_t* pempty = pfull + kWarps;     // ... and have been read
+  uint64_t* hfull = pempty + kWarps;     // an expert's rows of h are in shared memory
+  uint64_t* hempty = hfull + kHRing;     // ... and have been used by all of its stages
+  uint64_t* h_ready = hempty + kHRing;   // every CTA's h is written
+  uint64_t* x_done = h_ready + 1;        // x has been read for the last time
+  uint64_t* turns = x_done + 1;          // an adding warp's turn to take sums
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
   volatile int* n_list = abort_flag + 1;
   int* top_idx = reinterpret_cast<int*>(smem + L::kTopIdx);
@@ -442,23 +605,38 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParam
   int* prefix = reinterpret_cast<int*>(bits + 16);
   int* list = reinterpret_cast<int*>(smem + L::kList);
   uint32_t* used = reinterpret_cast<uint32_t*>(smem + L::kUsed);
+  int* first = reinterpret_cast<int*>(smem + L::kFirst);
   float* gates = reinterpret_cast<float*>(smem + L::kGate);
   float* red = reinterpret_cast<float*>(smem + L::kRed);
-  uint8_t* sx = smem + L::kX;
-  float* sxs = reinterpret_cast<float*>(sx + p.T * L::x_pitch(p.H));
+  float* down = reinterpret_cast<float*>(smem + L::kDown);
+  uint8_t* act = smem + L::kX;
   const int n_stages = p.n_stages;
-  uint8_t* scales = smem + L::scale_offset(p.T, p.H);
-  uint8_t* tiles = smem + L::tile_offset(p.T, p.H, n_stages);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int S = p.S, T = p.T, H = p.H, I = p.I;
+  uint8_t* scales = smem + L::scale_offset(T, H, I);
+  uint8_t* tiles = smem + L::tile_offset(T, H, I, n_stages);
   const int h_bytes = H * 2 / F::kPer2, i_bytes = I * 2 / F::kPer2;  // bytes of a W1/W3 and a W2 row
-  const int xp = L::x_pitch(H), xs = L::x_scales(H);
+  const int h_slabs = (h_bytes + F::kSlab - 1) / F::kSlab, i_slabs = (i_bytes + F::kSlab - 1) / F::kSlab;
+  const int xpitch = L::pitch(H), hpitch = L::pitch(I);
+  const int h_rows = L::act_bytes(T, H, I) / hpitch;  // rows of h that the activations' space holds, T at least
+  const DownRows dr = down_rows(p);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < n_stages; ++i) {
-      mbar_init(&full[i], kW == MOE_WDTYPE_FP8_E4M3 ? 33 : 1);
-      mbar_init(&empty[i], kWarps);
+      mbar_init(&full[i], kScaleBytes ? 2 : 1);
+      mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < kWarps; ++i) {
+      mbar_init(&pfull[i], 1);
+      mbar_init(&pempty[i], 1);
+    }
+    for (int i = 0; i < kHRing; ++i) {
+      mbar_init(&hfull[i], kPrep);
+      mbar_init(&hempty[i], dr.tiles ? dr.tiles * i_slabs : 1);
+    }
+    mbar_init(h_ready, 1);
+    mbar_init(x_done, kWarps);
+    for (int i = 0; i < kAcc; ++i) mbar_init(&turns[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -467,108 +645,47 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParam
   for (int i = threadIdx.x; i < kMaxU * kFewMaxTokens; i += kThreads) gates[i] = 0.0f;
   __syncthreads();
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer --
-    Ring rg;
-    uint32_t issued = 0, issued_phase = 0;
-    bool ok = p.inject != 1;
-    auto gate_up = [&](GateUpWalk w) {
-      Tile t;
-      while (ok && w.next(t)) {
-        const bool sh = S && t.u == 0;
-        const int e = sh ? 0 : list[t.u];
-        const int64_t blk = ((int64_t)e * (I / 128) + t.r0 / 128) * (H / 128);
-        const float* f0 = kW == MOE_WDTYPE_FP8_E4M3 ? (sh ? p.w.ss1 : p.w.s1) + blk : nullptr;
-        const float* f1 = kW == MOE_WDTYPE_FP8_E4M3 ? (sh ? p.w.ss3 : p.w.s3) + blk : nullptr;
-        ok = load_tile<kW>(
-            p, tiles, scales, full, empty, rg, 2, 8,
-            [&](int b) { return b == 0 ? (sh ? &tm.sw1 : &tm.w1) : (sh ? &tm.sw3 : &tm.w3); },
-            [&](int b) { return b == 0 ? (sh ? &tm.ss1 : &tm.s1) : (sh ? &tm.ss3 : &tm.s3); },
-            [&](int) { return e * I + t.r0; }, f0, f1, h_bytes, lane, abort_flag, issued, issued_phase);
-      }
-    };
-    gate_up(gate_up_walk(p, 0, S));  // the shared expert: needs no routing
-    named_bar_sync(1, kThreads);     // the expert list is ready
-    const int U = *n_list;
-    gate_up(gate_up_walk(p, S, U - S));
-    DownWalk dw = down_walk(p);
-    int r0, n;
-    while (ok && dw.next(r0, n)) {
-      for (int u = 0; u < U && ok; ++u) {
-        const bool sh = S && u == 0;
-        const int e = sh ? 0 : list[u];
-        const float* f = kW == MOE_WDTYPE_FP8_E4M3
-                             ? (sh ? p.w.ss2 : p.w.s2) + ((int64_t)e * (H / 128) + r0 / 128) * (I / 128)
-                             : nullptr;
-        ok = load_tile<kW>(
-            p, tiles, scales, full, empty, rg, n / 4, 4, [&](int) { return sh ? &tm.sw2 : &tm.w2; },
-            [&](int) { return sh ? &tm.ss2 : &tm.s2; }, [&](int b) { return e * H + r0 + 4 * b; }, f, f, i_bytes, lane,
-            abort_flag, issued, issued_phase);
-      }
-    }
-    if (kW == MOE_WDTYPE_FP8_E4M3) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0) {
-      // Let every copy land before the warp leaves (the consumers wait for them too, unless a wait gave up).
-      for (int s = 0; s < n_stages; ++s) {
-        if (!(issued & (1u << s))) continue;
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&full[s], (issued_phase >> s) & 1u) && global_timer_ns() - t0 < 200000000ull) {}
-      }
-    }
+  if (warp == kWarps + kAcc + kPrep) {
+    produce<kW, false>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, i_slabs, lane);
+    return;
+  }
+  if (warp == kWarps + kAcc + kPrep + 1) {
+    if constexpr (kScaleBytes)
+      produce<kW, true>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, i_slabs, lane);
+    else
+      named_bar_arrive(1, kThreads);
     return;
   }
 
-  // ------------------------------------------------------------- consumers --
   const int g = lane / 4, c = lane % 4;
-  // Activations into shared memory, in the operand layout. (x was complete
-  // before the router kernel passed its own wait.)
-  for (int t = 0; t < T; ++t) {
-    const uint4* xr = reinterpret_cast<const uint4*>(p.x) + (int64_t)t * (H / 8);
-    for (int v = threadIdx.x; v < H / 8; v += kConsumers) {  // H a multiple of 128: whole half-warps
-      const uint4 raw = __ldg(xr + v);
-      if constexpr (kW == MOE_WDTYPE_BF16) {
-        *reinterpret_cast<uint4*>(sx + t * xp + v * 16) = raw;
-      } else if constexpr (kW == MOE_WDTYPE_NVFP4) {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(&raw);
+  // Activations into shared memory, in the operand layout, 8 inputs per thread and
+  // step. (x was complete before the router kernel passed its own wait.)
+  constexpr int kUnroll = 4;
+  const int per_row = H / 8, nvec = T * per_row;  // a multiple of 16 per row: whole half-warps
+  for (int v0 = threadIdx.x; v0 - lane < nvec; v0 += kUnroll * kConsumers) {
+    uint4 raws[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint16_t*>(sx + t * xp + 2 * x_place<kW>(v * 8 + i)) = e[i];
-      } else {
-        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
-        float f[8];
+    for (int i = 0; i < kUnroll; ++i)
+      if (v0 + i * kConsumers < nvec) raws[i] = __ldg(reinterpret_cast<const uint4*>(p.x) + v0 + i * kConsumers);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 w2 = __bfloat1622float2(b[i]);
-          f[2 * i] = w2.x;
-          f[2 * i + 1] = w2.y;
-        }
-        const uint32_t act = H / 8 - (v - lane) >= 32 ? 0xffffffffu : 0xffffu;  // H/8 is a multiple of 16
-        uint32_t m = amax_bits<8>(f);
-        constexpr int kLanes = F::kBlock / 8;  // 16 (FP8) or 4 (MXFP4) lanes share a block
+    for (int i = 0; i < kUnroll; ++i) {
+      const int v = v0 + i * kConsumers;
+      if (v - lane >= nvec) break;
+      const bool live = v < nvec;
+      const uint4 raw = live ? raws[i] : make_uint4(0, 0, 0, 0);
+      const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
+      float f[8];
 #pragma unroll
-        for (int o = 1; o < kLanes; o *= 2) m = max(m, __shfl_xor_sync(act, m, o));
-        if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-          const float amax = __uint_as_float(m);
-          const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s)),
-                                            __NV_SATFINITE, __NV_E4M3);
-          *reinterpret_cast<uint4*>(sx + t * xp + v * 16) = make_uint4(f16x2_of_e4m3x2(w[0]), f16x2_of_e4m3x2(w[1]),
-                                                                       f16x2_of_e4m3x2(w[2]), f16x2_of_e4m3x2(w[3]));
-          if (v % kLanes == 0) sxs[t * xs + v / kLanes] = s;
-        } else {
-          const uint32_t sb = e8m0_of(m);
-          uint32_t h[4];
-          f16_of_e2m1x8(sb == 255u ? 0u : e2m1x8(f, e8m0_rcp(sb)), h);
-          *reinterpret_cast<uint4*>(sx + t * xp + v * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (v % kLanes == 0) sxs[t * xs + v / kLanes] = e8m0_value(sb);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float2 w2 = __bfloat1622float2(b[j]);
+        f[2 * j] = w2.x;
+        f[2 * j + 1] = w2.y;
       }
+      store_operand<kW, true>(act + v / per_row * xpitch, L::scales_at(H), v % per_row, f, live);
     }
   }
 
-  pdl_wait();  // the logits, the cleared counters
+  pdl_wait();  // the logits, the cleared counter
   if (warp < T) {
     // Top-k of token `warp`: order-preserving integer keys, ties to the lower
     // index, a NaN below everything; a taken expert's key is 0.
@@ -599,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParam
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (at == (uint32_t)(i * 32 + lane)) key[i] = 0;
-      const float l = __ldcg(p.logits + warp * p.E + at);
+      const float l = best == 1u ? __uint_as_float(0x7fffffffu)
+                                 : __uint_as_float((best >> 31) ? best ^ 0x80000000u : ~best);
       if (j == 0) l0 = l;
       if (lane == j) {
         w = l;
@@ -650,163 +768,286 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParam
     gates[u * kFewMaxTokens + t] = top_w[i];
     atomicOr(&used[u], 1u << t);
   }
-  // The expert list is ready. The producer waits for it here; the consumers do not
-  // wait for the producer, whose ring may be full of the shared expert's rows.
+  // The expert list is ready. The producers wait for it here; the consumers do not
+  // wait for the producers, whose ring may be full of the shared expert's rows.
   named_bar_arrive(1, kThreads);
   named_bar_sync(2, kConsumers);
   const int U = *n_list;
 
-  Ring rg;
+  // Stages are numbered in the producers' order; stage n is in ring slot n % n_stages
+  // and belongs to warp n % A, whose partial sums go to buffer n % A.
+  const int A = min(kWarps, n_stages);
+  const GateUpWalk walk0 = gate_up_walk(p, 0, S), walk1 = gate_up_walk(p, S, U - S);
+  const int tiles0 = walk0.end - walk0.pos;
+  const int gu_tiles = tiles0 + walk1.end - walk1.pos, gu_stages = gu_tiles * h_slabs;
+  const int per_entry = dr.tiles * i_slabs;  // stages of a list entry in the down phase
+  const int all_stages = gu_stages + U * per_entry;
   bool ok = true;
-  uint32_t buf = 0;
-  auto wait_full = [&] {
-    if (ok) ok = warp_wait<false>(&full[rg.stage], rg.phase, p.status, abort_flag, 0x2002, (int)buf, p.wait_ns);
-    return ok;
-  };
-  auto release = [&] {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[rg.stage]);
-    rg.step(n_stages);
-  };
-  const int xt = min(g, T - 1);  // lanes past the last token repeat it; their columns are not used
-  const int t0 = min(2 * c, T - 1), t1 = min(2 * c + 1, T - 1);
 
-  // ---- gate/up ----
-  auto gate_up = [&](GateUpWalk w) {
-    Tile t;
-    while (w.next(t)) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k0 = 0; k0 < h_bytes; k0 += kSlab) {
-        const int chunks = min(kSlab, h_bytes - k0) / kChunk;
-        if (wait_full()) {
-          const Rows rows{tiles + rg.stage * (kRows * kSlab), scales + rg.stage * L::kStageScales, g * 128,
-                          8 * kSlab + g * 128, 8 * 128};
-          for (int q = warp; q < chunks; q += kWarps) {
-            const int kq = k0 / kChunk + q;
-            XFrag<kW> x;
-#pragma unroll
-            for (int i = 0; i < XFrag<kW>::kVecs; ++i)
-              x.v[i] = *reinterpret_cast<const uint4*>(sx + xt * xp + frag_offset<kW>(kq, c, i));
-            float sb0 = 1.0f, sb1 = 1.0f;
-            if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-              x.s0[0] = sxs[t0 * xs + kq / 2];
-              x.s1[0] = sxs[t1 * xs + kq / 2];
-              const float* fs = reinterpret_cast<const float*>(rows.scales);
-              sb0 = fs[q / 2];
-              sb1 = fs[8 + q / 2];
-            } else if constexpr (kW == MOE_WDTYPE_MXFP4) {
-              *reinterpret_cast<float4*>(x.s0) = *reinterpret_cast<const float4*>(sxs + t0 * xs + kq * 4);
-              *reinterpret_cast<float4*>(x.s1) = *reinterpret_cast<const float4*>(sxs + t1 * xs + kq * 4);
-            }
-            chunk_mma<kW>(acc, rows, q, x, sb0, sb1, lane);
-          }
-        }
-        release();
+  if (warp < kWarps) {
+    // ------------------------------------------------------------ multiply --
+    Ring rg, pr;  // this warp's next ring slot; phase of its buffer
+    auto advance = [&](int n) {
+      rg.stage += n;
+      while (rg.stage >= n_stages) {
+        rg.stage -= n_stages;
+        rg.phase ^= 1u;
       }
-      float* part = red + (buf & 1u) * (kWarps * 128);
-      *reinterpret_cast<float4*>(part + warp * 128 + lane * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      named_bar_sync(2, kConsumers);
-      // One warp finishes the tile (each in turn): lane (g, c) sums feature g of tokens 2c, 2c + 1.
-      if (warp == (int)(buf % kWarps)) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(part + i * 128 + lane * 4);
-          s[0] += v.x;
-          s[1] += v.y;
-          s[2] += v.z;
-          s[3] += v.w;
-        }
-        if constexpr (kW == MOE_WDTYPE_NVFP4) {
-          const bool sh = S && t.u == 0;
-          const int e = sh ? 0 : list[t.u];
-          const float f1 = (sh ? p.w.sg1 : p.w.g1)[e] * 256.0f, f3 = (sh ? p.w.sg3 : p.w.g3)[e] * 256.0f;
-          s[0] *= f1;
-          s[1] *= f1;
-          s[2] *= f3;
-          s[3] *= f3;
-        }
-        const uint32_t mask = used[t.u];
-        const int f = t.r0 + g;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int tok = 2 * c + j;
-          if ((mask >> tok) & 1u) {
-            const float h = silu_mul(s[j], s[2 + j]);
-            const int64_t row = (int64_t)t.u * kFewMaxTokens + tok;
-            if constexpr (F::kBlock == 0)
-              p.hq[row * I + x_place<kW>(f)] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
-            else
-              __stcg(p.h + row * I + f, h);
-          }
-        }
-        if constexpr (F::kBlock != 0) {
-          // Whoever completes a block quantises it for the tokens that use it.
-          __syncwarp();
-          const int b = t.r0 / F::kBlock;
-          int old = 0;
-          if (lane == 0) {
-            __threadfence();
-            old = atomicAdd(&p.counters[1 + t.u * (I / F::kBlock) + b], 8);
-          }
-          old = __shfl_sync(0xffffffffu, old, 0);
-          if (old + 8 == F::kBlock) {
-            __threadfence();
-            for (uint32_t mm = mask; mm; mm &= mm - 1) {
-              const int64_t row = (int64_t)t.u * kFewMaxTokens + __ffs(mm) - 1;
-              if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.h + row * I + b * 128) + lane);
-                float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-                uint32_t nan = (isnan(v.x) || isnan(v.y) || isnan(v.z) || isnan(v.w)) ? 1u : 0u;
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                nan = __any_sync(0xffffffffu, nan);
-                const float sc = nan ? __uint_as_float(0x7fffffffu) : amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-                const float inv = amax > 0.0f ? __frcp_rn(sc) : 0.0f;
-                const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v.x * inv, v.y * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(v.z * inv, v.w * inv), __NV_SATFINITE, __NV_E4M3);
-                reinterpret_cast<uint2*>(p.hq + row * I + b * 128)[lane] =
-                    make_uint2(f16x2_of_e4m3x2(a), f16x2_of_e4m3x2(d));
-                if (lane == 0) p.hs[row * (I / 128) + b] = sc;
-              } else {
-                // Four lanes, 8 features each.
-                float v[8];
-                if (lane < 4) {
-                  *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(p.h + row * I + b * 32) + 2 * lane);
-                  *reinterpret_cast<float4*>(v + 4) =
-                      __ldcg(reinterpret_cast<const float4*>(p.h + row * I + b * 32) + 2 * lane + 1);
-                }
-                uint32_t m = lane < 4 ? amax_bits<8>(v) : 0u;
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const uint32_t sb = e8m0_of(m);
-                if (lane < 4) {
-                  uint32_t hv[4];
-                  f16_of_e2m1x8(sb == 255u ? 0u : e2m1x8(v, e8m0_rcp(sb)), hv);
-                  *reinterpret_cast<uint4*>(p.hq + row * I + b * 32 + lane * 8) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-                  if (lane == 0) p.hs[row * (I / 32) + b] = e8m0_value(sb);
-                }
-              }
-            }
-          }
+    };
+    advance(warp);
+    // FP8: a stage's weight scales: lane l < 8 holds that of rows 0..7 (down: of the
+    // tile's first row's block) and K block l, lane 8 + l that of rows 8..15 (of its
+    // last row's block); fetched a turn ahead.
+    auto fetch_scale = [&](int m) {
+      if (kW != MOE_WDTYPE_FP8_E4M3 || m >= all_stages || lane >= 16) return 0.0f;
+      const int l = lane % 8;
+      const float* f;
+      int kb;
+      if (m < gu_stages) {
+        const int tile = m / h_slabs;
+        GateUpWalk w = tile < tiles0 ? walk0 : walk1;
+        w.pos += tile < tiles0 ? tile : tile - tiles0;
+        Tile t;
+        w.next(t);
+        const bool sh = S && t.u == 0;
+        kb = m % h_slabs * 8 + l;
+        if (kb >= H / 128) return 0.0f;
+        f = (lane < 8 ? (sh ? p.w.ss1 : p.w.s1) : (sh ? p.w.ss3 : p.w.s3)) +
+            ((int64_t)(sh ? 0 : list[t.u]) * (I / 128) + t.r0 / 128) * (H / 128);
+      } else {
+        m -= gu_stages;
+        const int u = down_entry(m / per_entry, U, S), tile = m % per_entry / i_slabs;
+        const bool sh = S && u == 0;
+        kb = m % i_slabs * 8 + l;
+        if (kb >= I / 128) return 0.0f;
+        const int row = dr.first(tile) + (lane < 8 ? 0 : dr.count(tile) - 1);
+        f = (sh ? p.w.ss2 : p.w.s2) + ((int64_t)(sh ? 0 : list[u]) * (H / 128) + row / 128) * (I / 128);
+      }
+      return __ldg(f + kb);
+    };
+    float next_scale = warp < A ? fetch_scale(warp) : 0.0f;
+    bool x_used = true;
+    for (int n = warp; n < all_stages && warp < A; n += A) {
+      const float scale = next_scale;
+      next_scale = fetch_scale(n + A);
+      const bool gate_up = n < gu_stages;
+      if (!gate_up && x_used) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_done);
+        x_used = false;
+      }
+      // The stage's K range, the token rows, and where the weight rows lie: in boxes
+      // of eight rows, or of four.
+      int k0, row_bytes, entry = 0, sel0 = 0, sel1 = 8;
+      Operands o;
+      if (gate_up) {
+        k0 = n % h_slabs * F::kSlab;
+        row_bytes = h_bytes;
+        o.x = act + min(g, T - 1) * xpitch;  // lanes past the last token repeat it; their columns are not used
+        o.s0 = reinterpret_cast<const float*>(act + min(2 * c, T - 1) * xpitch + L::scales_at(H));
+        o.s1 = reinterpret_cast<const float*>(act + min(2 * c + 1, T - 1) * xpitch + L::scales_at(H));
+        o.r0 = g * 128;
+        o.step = 8 * 128;
+      } else {
+        const int m = n - gu_stages, u = down_entry(m / per_entry, U, S), tile = m % per_entry / i_slabs;
+        entry = m / per_entry;
+        k0 = m % i_slabs * F::kSlab;
+        row_bytes = i_bytes;
+        if (ok)
+          ok = warp_wait<false>(&hfull[entry % kHRing], (uint32_t)(entry / kHRing) & 1u, p.status, abort_flag, 0x2005, n,
+                                p.wait_ns);
+        // Row of a token that uses the expert; the other columns repeat its first row and
+        // are not used. (first[] is complete before any entry is.)
+        const uint32_t mask = used[u];
+        const int row0 = ok ? first[entry] : 0;
+        auto row_of = [&](int tok) {
+          const int r = (mask >> tok) & 1u ? __popc(mask & ((1u << tok) - 1u)) : 0;
+          return act + (row0 + r) % h_rows * hpitch;
+        };
+        o.x = row_of(g);
+        o.s0 = reinterpret_cast<const float*>(row_of(2 * c) + L::scales_at(I));
+        o.s1 = reinterpret_cast<const float*>(row_of(2 * c + 1) + L::scales_at(I));
+        o.r0 = (g / 4) * 4 * F::kSlab + (g % 4) * 128;
+        o.step = 4 * 128;
+        if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+          const int top = dr.first(tile) / 128;
+          sel0 = (dr.first(tile) + g) / 128 != top ? 8 : 0;
+          sel1 = (dr.first(tile) + g + 8) / 128 != top ? 8 : 0;
         }
       }
-      ++buf;
+      o.r1 = o.r0 + 8 * F::kSlab;
+      const int lines = min(F::kSlab, row_bytes - k0) / kLine, kl0 = k0 / kLine;
+      Sums acc;
+      acc.clear();
+      // Stage n's slot held stage n - n_stages before, which another warp may not even
+      // have seen land: its release is waited for first, or the parity of `full` could
+      // be taken for the phase before. (The release before that one is certain: stage
+      // n - A was loaded, so every stage up to n - A - n_stages has been released, and
+      // A <= n_stages.)
+      if (ok) ok = warp_wait<false>(&empty[rg.stage], rg.phase ^ 1u, p.status, abort_flag, 0x2007, n, p.wait_ns);
+      if (ok) ok = warp_wait<false>(&full[rg.stage], rg.phase, p.status, abort_flag, 0x2002, n, p.wait_ns);
+      if (ok) {
+        o.tile = tiles + rg.stage * (kRows * F::kSlab);
+        o.scales = scales + rg.stage * L::kStageScales;
+#pragma unroll(kW == MOE_WDTYPE_BF16 || kW == MOE_WDTYPE_FP8_E4M3 ? 2 : 1)
+        for (int l = 0; l < lines; ++l) {
+          float sb0 = 1.0f, sb1 = 1.0f;
+          if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+            sb0 = __shfl_sync(0xffffffffu, scale, sel0 + l);
+            sb1 = __shfl_sync(0xffffffffu, scale, sel1 + l);
+          }
+          line_mma<kW>(acc, o, l, kl0 + l, sb0, sb1, lane);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&empty[rg.stage]);
+        if (!gate_up) mbar_arrive(&hempty[entry % kHRing]);
+      }
+      advance(A);
+      if (ok) ok = warp_wait<false>(&pempty[warp], pr.phase ^ 1u, p.status, abort_flag, 0x2004, n, p.wait_ns);
+      *reinterpret_cast<float4*>(red + warp * 128 + lane * 4) = acc.total();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[warp]);
+      pr.phase ^= 1u;
     }
-  };
-  gate_up(gate_up_walk(p, 0, S));
-  gate_up(gate_up_walk(p, S, U - S));
+    if (x_used) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_done);
+    }
+    return;
+  }
 
-  // ---- grid barrier: every h is written ----
+  if (warp >= kWarps + kAcc) {
+    // ------------------------------------------------------- h for the down phase --
+    // The rows of a list entry's tokens lie one after another in the activations'
+    // space, entries following entries around it (first[] counts the rows).
+    const int me = warp - kWarps - kAcc;
+    if (dr.tiles == 0) return;  // no rows of the output here
+    if (me == 0 && lane == 0) {
+      int rows = 0;
+      for (int i = 0; i < U; ++i) {
+        first[i] = rows;
+        rows += __popc(used[down_entry(i, U, S)]);
+      }
+    }
+    named_bar_sync(4, kPrep * 32);
+    if (ok) ok = warp_wait<false>(x_done, 0, p.status, abort_flag, 0x200a, 0, p.wait_ns);
+    if (ok) ok = warp_wait<false>(h_ready, 0, p.status, abort_flag, 0x200b, 0, p.wait_ns);
+    int freed = 0;  // entries whose rows are free again
+    for (int i = 0; i < U; ++i) {
+      const int u = down_entry(i, U, S);
+      uint32_t mask = used[u];
+      const int end = first[i] + __popc(mask);
+      // (first[] counts on from entry to entry, so the oldest rows go first.)
+      while (ok && (freed <= i - kHRing || first[freed] < end - h_rows)) {
+        ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c, i,
+                              p.wait_ns);
+        ++freed;
+      }
+      for (int r = 0; mask; ++r, mask &= mask - 1) {
+        if ((first[i] + r) % kPrep != me) continue;
+        const float4* src =
+            reinterpret_cast<const float4*>(p.h + ((int64_t)u * kFewMaxTokens + __ffs(mask) - 1) * I);
+        uint8_t* row = act + (first[i] + r) % h_rows * hpitch;
+        constexpr int kBatch = 6;
+        for (int v0 = lane; v0 - lane < I / 8; v0 += 32 * kBatch) {
+          float4 raw[2 * kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            if (v0 + 32 * j >= I / 8) continue;
+            raw[2 * j] = __ldcg(src + 2 * (v0 + 32 * j));
+            raw[2 * j + 1] = __ldcg(src + 2 * (v0 + 32 * j) + 1);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int v = v0 + 32 * j;
+            if (v - lane >= I / 8) break;
+            const bool live = v < I / 8;
+            const float4 a = live ? raw[2 * j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 b = live ? raw[2 * j + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            store_operand<kW, false>(row, L::scales_at(I), v, f, live);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hfull[i % kHRing]);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ add up --
+  // Lane (g, c) holds rows g and g + 8 of tokens 2c, 2c + 1. The warps take the
+  // sums of the tiles strictly in turn, so that a buffer's parity is never that of
+  // an earlier stage, and finish them side by side.
+  const int me = warp - kWarps;
+  int n = 0, turn = 0;
+  uint32_t turn_phase = 0;
+  auto take = [&](float (&s)[4]) {  // stage n's partial sums
+    const int w = n % A;
+    if (ok) ok = warp_wait<false>(&pfull[w], (uint32_t)(n / A) & 1u, p.status, abort_flag, 0x2006, n, p.wait_ns);
+    const float4 v = *reinterpret_cast<const float4*>(red + w * 128 + lane * 4);
+    s[0] += v.x;
+    s[1] += v.y;
+    s[2] += v.z;
+    s[3] += v.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&pempty[w]);
+    ++n;
+  };
+  auto begin_turn = [&] {
+    if (turn == 0) return;
+    if (ok) ok = warp_wait<false>(&turns[me], turn_phase, p.status, abort_flag, 0x2009, n, p.wait_ns);
+    turn_phase ^= 1u;
+  };
+  auto end_turn = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&turns[(me + 1) % kAcc]);
+  };
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    GateUpWalk w = part == 0 ? walk0 : walk1;
+    Tile t;
+    for (; w.next(t); ++turn) {
+      if (turn % kAcc != me) {
+        n += h_slabs;
+        continue;
+      }
+      begin_turn();
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < h_slabs; ++k) take(s);
+      end_turn();
+      if constexpr (kW == MOE_WDTYPE_NVFP4) {
+        const bool sh = S && t.u == 0;
+        const int e = sh ? 0 : list[t.u];
+        const float f1 = (sh ? p.w.sg1 : p.w.g1)[e], f3 = (sh ? p.w.sg3 : p.w.g3)[e];
+        s[0] *= f1;
+        s[1] *= f1;
+        s[2] *= f3;
+        s[3] *= f3;
+      }
+      const uint32_t mask = used[t.u];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tok = 2 * c + j;
+        if ((mask >> tok) & 1u)
+          __stcg(p.h + ((int64_t)t.u * kFewMaxTokens + tok) * I + t.r0 + g, silu_mul(s[j], s[2 + j]));
+      }
+    }
+  }
+
+  // Grid barrier: every h is written.
   __threadfence();
-  named_bar_sync(2, kConsumers);
-  if (threadIdx.x == 0) {
-    atomicAdd(&p.counters[0], 1);
+  named_bar_sync(3, kAcc * 32);
+  if (me == 0 && lane == 0) {
+    __threadfence();
+    atomicAdd(p.counter, 1);
     const uint64_t start = global_timer_ns();
     uint32_t spins = 0;
     while (true) {
       int v;
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p.counters) : "memory");
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p.counter) : "memory");
       if (v >= (int)gridDim.x) break;
       if ((++spins & 63u) == 0 && (*abort_flag || global_timer_ns() - start > p.wait_ns)) {
         if (!*abort_flag) latch_timeout(p.status, 0x2003, v);
@@ -815,102 +1056,54 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const FewParam
       }
     }
     __threadfence();
+    mbar_arrive(h_ready);
   }
-  named_bar_sync(2, kConsumers);
 
-  // ---- down ----
-  DownWalk dw = down_walk(p);
-  int r0, n;
-  while (dw.next(r0, n)) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int u = 0; u < U; ++u) {
-      const uint32_t mask = used[u];
-      const float g0 = gates[u * kFewMaxTokens + 2 * c], g1 = gates[u * kFewMaxTokens + 2 * c + 1];
-      const bool on = (mask >> g) & 1u, on0 = (mask >> (2 * c)) & 1u, on1 = (mask >> (2 * c + 1)) & 1u;
-      const int64_t row = (int64_t)u * kFewMaxTokens;
-      const uint8_t* hrow = reinterpret_cast<const uint8_t*>(p.hq + (row + g) * I);
+  // Down: one warp adds up, entry by entry; a token without the expert takes nothing
+  // from it, whatever its weights hold.
+  if (me != turn % kAcc) return;
+  begin_turn();
+  for (int i = lane; i < dr.tiles * 128; i += 32) down[i] = 0.0f;
+  __syncwarp();
+  for (int i = 0; i < U; ++i) {
+    const int u = down_entry(i, U, S);
+    const uint32_t mask = used[u];
+    float s = 1.0f;
+    if constexpr (kW == MOE_WDTYPE_NVFP4) s = (S && u == 0) ? p.w.sg2[0] : p.w.g2[list[u]];
+    const float g0 = s * gates[u * kFewMaxTokens + 2 * c], g1 = s * gates[u * kFewMaxTokens + 2 * c + 1];
+    for (int tile = 0; tile < dr.tiles; ++tile) {
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k0 = 0; k0 < i_bytes; k0 += kSlab) {
-        const int chunks = min(kSlab, i_bytes - k0) / kChunk;
-        constexpr int kPer = kSlab / kChunk / kWarps;
-        // This stage's activations, before the wait for its weights.
-        XFrag<kW> x[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int q = warp + j * kWarps, kq = k0 / kChunk + q;
-          const bool live = q < chunks;
-#pragma unroll
-          for (int i = 0; i < XFrag<kW>::kVecs; ++i)
-            x[j].v[i] = live && on ? __ldcg(reinterpret_cast<const uint4*>(hrow + frag_offset<kW>(kq, c, i)))
-                                   : make_uint4(0, 0, 0, 0);
-          if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-            x[j].s0[0] = live && on0 ? __ldcg(p.hs + (row + 2 * c) * (I / 128) + kq / 2) : 0.0f;
-            x[j].s1[0] = live && on1 ? __ldcg(p.hs + (row + 2 * c + 1) * (I / 128) + kq / 2) : 0.0f;
-          } else if constexpr (kW == MOE_WDTYPE_MXFP4) {
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(x[j].s0) =
-                live && on0 ? __ldcg(reinterpret_cast<const float4*>(p.hs + (row + 2 * c) * (I / 32) + kq * 4)) : z;
-            *reinterpret_cast<float4*>(x[j].s1) =
-                live && on1 ? __ldcg(reinterpret_cast<const float4*>(p.hs + (row + 2 * c + 1) * (I / 32) + kq * 4)) : z;
-          }
-        }
-        if (wait_full()) {
-          // Boxes of four rows.
-          const int r = (g / 4) * 4 * kSlab + (g % 4) * 128;
-          const Rows rows{tiles + rg.stage * (kRows * kSlab), scales + rg.stage * L::kStageScales, r, r + 8 * kSlab,
-                          4 * 128};
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int q = warp + j * kWarps;
-            if (q >= chunks) break;
-            float sb = 1.0f;
-            if constexpr (kW == MOE_WDTYPE_FP8_E4M3)
-              sb = reinterpret_cast<const float*>(rows.scales)[q / 2];
-            chunk_mma<kW>(d, rows, q, x[j], sb, sb, lane);
-          }
-        }
-        release();
+      for (int k = 0; k < i_slabs; ++k) take(d);
+      float4* at = reinterpret_cast<float4*>(down + tile * 128 + lane * 4);
+      float4 acc = *at;
+      if ((mask >> (2 * c)) & 1u) {
+        acc.x = fmaf(d[0], g0, acc.x);
+        acc.z = fmaf(d[2], g0, acc.z);
       }
-      float s = 1.0f;
-      if constexpr (kW == MOE_WDTYPE_NVFP4) s = ((S && u == 0) ? p.w.sg2[0] : p.w.g2[list[u]]) * 256.0f;
-      // A token without this expert takes nothing from it, whatever its weights hold.
-      if (on0) {
-        acc[0] = fmaf(d[0], s * g0, acc[0]);
-        acc[2] = fmaf(d[2], s * g0, acc[2]);
+      if ((mask >> (2 * c + 1)) & 1u) {
+        acc.y = fmaf(d[1], g1, acc.y);
+        acc.w = fmaf(d[3], g1, acc.w);
       }
-      if (on1) {
-        acc[1] = fmaf(d[1], s * g1, acc[1]);
-        acc[3] = fmaf(d[3], s * g1, acc[3]);
-      }
+      *at = acc;
     }
-    float* part = red + (buf & 1u) * (kWarps * 128);
-    *reinterpret_cast<float4*>(part + warp * 128 + lane * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    named_bar_sync(2, kConsumers);
-    if (warp == (int)(buf % kWarps) && ok) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+  }
+  if (!ok || *abort_flag) return;
+  for (int tile = 0; tile < dr.tiles; ++tile) {
+    const float4 acc = *reinterpret_cast<const float4*>(down + tile * 128 + lane * 4);
+    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(part + i * 128 + lane * 4);
-        s[0] += v.x;
-        s[1] += v.y;
-        s[2] += v.z;
-        s[3] += v.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = g + 8 * (j / 2), tok = 2 * c + j % 2;
-        if (r < n && tok < T) p.out[(int64_t)tok * H + r0 + r] = __float2bfloat16_rn(s[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int r = g + 8 * (j / 2), tok = 2 * c + j % 2;
+      if (r < dr.count(tile) && tok < T) p.out[(int64_t)tok * H + dr.first(tile) + r] = __float2bfloat16_rn(v[j]);
     }
-    ++buf;
   }
 }
 
 template <int kW>
 cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) {
   auto kern = few_experts_kernel<kW>;
-  p.n_stages = Smem<kW>::stages(p.T, p.H);
-  const int smem = Smem<kW>::tile_offset(p.T, p.H, p.n_stages) + p.n_stages * kRows * kSlab + 1024;
+  p.n_stages = Smem<kW>::stages(p.T, p.H, p.I);
+  const int smem = Smem<kW>::tile_offset(p.T, p.H, p.I, p.n_stages) + p.n_stages * kRows * Fmt<kW>::kSlab + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(few_router_kernel, dim3((unsigned)p.E), dim3(kRouterThreads), 0, s, 1, p);
@@ -932,24 +1125,20 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
 }
 
 template <int kW>
-bool fits(int T, int H) {
-  return Smem<kW>::stages(T, H) >= 3;
+bool fits(int T, int H, int I, int sms) {
+  // A ring of some stages, and the output sums of a CTA's rows.
+  return Smem<kW>::stages(T, H, I) >= 3 && ceil_div(ceil_div(H / 4, sms) * 4, 16) <= kFewDownTiles;
 }
 
 }  // namespace
 
-bool few_fits(int wdtype, int T, int H) {
+bool few_fits(int wdtype, int T, int H, int I, int sms) {
   switch (wdtype) {
-    case MOE_WDTYPE_BF16: return fits<MOE_WDTYPE_BF16>(T, H);
-    case MOE_WDTYPE_FP8_E4M3: return fits<MOE_WDTYPE_FP8_E4M3>(T, H);
-    case MOE_WDTYPE_NVFP4: return fits<MOE_WDTYPE_NVFP4>(T, H);
-    default: return fits<MOE_WDTYPE_MXFP4>(T, H);
+    case MOE_WDTYPE_BF16: return fits<MOE_WDTYPE_BF16>(T, H, I, sms);
+    case MOE_WDTYPE_FP8_E4M3: return fits<MOE_WDTYPE_FP8_E4M3>(T, H, I, sms);
+    case MOE_WDTYPE_NVFP4: return fits<MOE_WDTYPE_NVFP4>(T, H, I, sms);
+    default: return fits<MOE_WDTYPE_MXFP4>(T, H, I, sms);
   }
-}
-
-int few_counters(int wdtype, int T, int k, int S, int I) {
-  const int block = wdtype == MOE_WDTYPE_FP8_E4M3 ? 128 : wdtype == MOE_WDTYPE_MXFP4 ? 32 : 0;
-  return 1 + (block ? (T * k + S) * (I / block) : 0);
 }
 
 cudaError_t launch_few(const FewParams& p, const FewMaps& tm, int wdtype, int sms, cudaStream_t s) {

@@ -9,11 +9,11 @@ namespace moe {
 
 constexpr int kFewMaxTokens = MOE_FEW_MAX_TOKENS;
 constexpr int kFewSmem = 227 * 1024;  // shared memory of a CTA
+constexpr int kFewDownTiles = 16;     // 16-row tiles of the output that a CTA may own
 
 struct FewParams {
   int32_t T, H, I, E, k, S;
   int32_t n_stages;        // weight ring (set by the launcher)
-  int32_t n_counters;
   const uint16_t* x;       // [T, H] bf16
   const uint16_t* router_w;
   const float* bias;       // [E] or null
@@ -22,27 +22,22 @@ struct FewParams {
   int32_t* topk_idx;       // [T, k] or null
   float* topk_w;
   float* logits;           // [T, E]
-  // Per (list entry, token): h as fp32 before quantisation (FP8, MXFP4), as the
-  // down products read it, and its block scales.
-  float* h;
-  uint16_t* hq;
-  float* hs;
-  int* counters;           // [0] grid barrier, [1..] features done per block
+  float* h;                // [list entries, 8, I]
+  int* counter;            // grid barrier
   int* status;
   uint64_t wait_ns;
   int32_t inject;
 };
 
 // Weight tensor maps: rows as [128 bytes, rows, lines], boxes of 128 bytes x 8 rows
-// (w1, w3) or 4 rows (w2) x 8 lines, 128B-swizzled; 4-bit storage: scale bytes
-// [rows, K / block] in boxes of the same rows x a 1024-byte slab's scales.
+// (w1, w3) or 4 rows (w2) x a slab's 8 (BF16, FP8) or 4 lines, 128B-swizzled; 4-bit
+// storage: scale bytes [rows, K / block] in boxes of the same rows x a slab's scales.
 struct FewMaps {
   CUtensorMap w1, w3, w2, sw1, sw3, sw2, s1, s3, s2, ss1, ss3, ss2;
 };
 
-// Whether T tokens of H inputs leave room for the weight ring.
-bool few_fits(int wdtype, int T, int H);
-int few_counters(int wdtype, int T, int k, int S, int I);
+// Whether T tokens leave room for the weight ring in shared memory.
+bool few_fits(int wdtype, int T, int H, int I, int sms);
 cudaError_t launch_few(const FewParams& p, const FewMaps& tm, int wdtype, int sms, cudaStream_t s);
 
 }  // namespace moe
