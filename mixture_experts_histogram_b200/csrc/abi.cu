@@ -713,6 +713,7 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   if (T > 0 && T <= MOE_FEW_MAX_TOKENS) {
     // The few-token layer: list entries x 8 token slots of h.
     L.few_counter = take(4);
+    L.few_x = take((size_t)few_x_bytes(c.wdtype, (int)T, c.hidden));
     L.few_h = take((size_t)(T * k + S) * MOE_FEW_MAX_TOKENS * c.inter * 4);
   }
   L.total = off;
@@ -789,6 +790,7 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.topk_idx = topk_idx;
   p.topk_w = topk_w;
   p.logits = reinterpret_cast<float*>(ws + L.logits_part);
+  p.xrows = ws + L.few_x;
   p.h = reinterpret_cast<float*>(ws + L.few_h);
   p.counter = reinterpret_cast<int*>(ws + L.few_counter);
   p.status = reinterpret_cast<int*>(ws + L.status);

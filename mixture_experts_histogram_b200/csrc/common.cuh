@@ -29,7 +29,7 @@ struct WsLayout {
   int64_t T, R, rows_pad, chunks, ksplit;
   size_t status, idx, gate, logits_part, chunk_base, counts, offsets, mt_prefix, mp_prefix;
   size_t perm, pos, row_gate, xp, sxp, h, sh, y, part, x_stage, out_stage;
-  size_t few_counter, few_h;  // T <= MOE_FEW_MAX_TOKENS only
+  size_t few_counter, few_x, few_h;  // T <= MOE_FEW_MAX_TOKENS only
   size_t total;
 };
 

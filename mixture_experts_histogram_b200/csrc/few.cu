@@ -86,7 +86,7 @@ struct Smem {
   // Fixed part: barriers, tables, partial sums. Then the activations (x, later rows
   // of h), the scale bytes and the weight tiles.
   static constexpr int kBars = 0;
-  static constexpr int kNumBars = 2 * kMaxRing + 2 * kWarps + 2 * kHRing + 2 + kAcc;
+  static constexpr int kNumBars = 2 * kMaxRing + 2 * kWarps + 2 * kHRing + 3 + kAcc;
   static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;  // abort flag, list length
   static constexpr int kTopIdx = kMisc + 64;                         // int [8][16]
   static constexpr int kTopW = kTopIdx + kFewMaxTokens * kMaxTopK * 4;
@@ -104,10 +104,12 @@ struct Smem {
   static __host__ __device__ int pitch(int K) {
     return F::kBlock ? (scales_at(K) + K / F::kBlock * 4 + 63) / 128 * 128 + 64 + (F::kXPad == 16 ? 16 : 0) : scales_at(K);
   }
-  // Bytes for T rows of x, then as many rows of h as fit, T at least.
+  // Bytes for T rows of x, and then for rows of h: T at least, and up to a dozen so
+  // that the next experts' can be brought while one is used.
   static __host__ __device__ int act_bytes(int T, int H, int I) {
-    const int x = T * pitch(H), h = T * pitch(I);
-    return x > h ? x : h;
+    const int x = T * pitch(H), some = 40 * 1024 / pitch(I), rows = some > 12 ? 12 : some;
+    const int h = (rows > T ? rows : T) * pitch(I);
+    return (x > h ? x : h);
   }
   static __host__ __device__ int scale_offset(int T, int H, int I) {
     return (kX + act_bytes(T, H, I) + 127) / 128 * 128;
@@ -120,54 +122,6 @@ struct Smem {
     return n > kMaxRing ? kMaxRing : n;
   }
 };
-
-// ------------------------------------------------------------------ router --
-
-// One CTA per expert: logits [T, E] of all tokens, fp32 sums in a fixed order.
-// CTA 0 also clears the status record and the second kernel's barrier counter.
-__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewParams p) {
-  pdl_wait();
-  pdl_trigger();  // after the wait: the next kernel may read everything that this one may
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < (int)(kStatusBytes / 4); i += kRouterThreads) p.status[i] = 0;
-    if (threadIdx.x == 0) *p.counter = 0;
-  }
-  __shared__ float part[kRouterThreads / 32][kFewMaxTokens];
-  const int e = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (int64_t)e * (p.H / 8);
-  float acc[kFewMaxTokens];
-#pragma unroll
-  for (int t = 0; t < kFewMaxTokens; ++t) acc[t] = 0.0f;
-  for (int v = threadIdx.x; v < p.H / 8; v += kRouterThreads) {
-    const uint4 wv = __ldg(w + v);
-    const __nv_bfloat162* wb = reinterpret_cast<const __nv_bfloat162*>(&wv);
-#pragma unroll
-    for (int t = 0; t < kFewMaxTokens; ++t) {
-      if (t >= p.T) break;
-      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)t * (p.H / 8) + v);
-      const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(&xv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = __bfloat1622float2(wb[i]), b = __bfloat1622float2(xb[i]);
-        acc[t] = fmaf(a.x, b.x, acc[t]);
-        acc[t] = fmaf(a.y, b.y, acc[t]);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < kFewMaxTokens; ++t) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-    if (lane == 0) part[warp][t] = acc[t];
-  }
-  __syncthreads();
-  if (threadIdx.x < p.T) {
-    float l = 0.0f;
-    for (int i = 0; i < kRouterThreads / 32; ++i) l += part[i][threadIdx.x];
-    if (p.bias) l += p.bias[e];
-    p.logits[threadIdx.x * p.E + e] = l;
-  }
-}
 
 // ------------------------------------------------------------------- pieces --
 
@@ -435,7 +389,89 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
   }
 }
 
+// ------------------------------------------------------------------ router --
+
+// One CTA per expert: logits [T, E] of all tokens, fp32 sums in a fixed order. The
+// CTAs after those bring x into the operand layout, rows of Smem::pitch(H) bytes.
+// CTA 0 also clears the status record and the second kernel's barrier counter.
+template <int kW>
+__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewParams p) {
+  using L = Smem<kW>;
+  pdl_wait();
+  pdl_trigger();  // after the wait: the next kernel may read everything that this one may
+  if ((int)blockIdx.x >= p.E) {
+    const int per_row = p.H / 8, v = ((int)blockIdx.x - p.E) * kRouterThreads + threadIdx.x;  // 16 k per row
+    const bool live = v < p.T * per_row;
+    const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(p.x) + v) : make_uint4(0, 0, 0, 0);
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 w2 = __bfloat1622float2(b[j]);
+      f[2 * j] = w2.x;
+      f[2 * j + 1] = w2.y;
+    }
+    store_operand<kW, true>(p.xrows + v / per_row * L::pitch(p.H), L::scales_at(p.H), v % per_row, f, live);
+    return;
+  }
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < (int)(kStatusBytes / 4); i += kRouterThreads) p.status[i] = 0;
+    if (threadIdx.x == 0) *p.counter = 0;
+  }
+  __shared__ float part[kRouterThreads / 32][kFewMaxTokens];
+  const int e = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (int64_t)e * (p.H / 8);
+  float acc[kFewMaxTokens];
+#pragma unroll
+  for (int t = 0; t < kFewMaxTokens; ++t) acc[t] = 0.0f;
+  for (int v = threadIdx.x; v < p.H / 8; v += kRouterThreads) {
+    const uint4 wv = __ldg(w + v);
+    const __nv_bfloat162* wb = reinterpret_cast<const __nv_bfloat162*>(&wv);
+#pragma unroll
+    for (int t = 0; t < kFewMaxTokens; ++t) {
+      if (t >= p.T) break;
+      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)t * (p.H / 8) + v);
+      const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(&xv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = __bfloat1622float2(wb[i]), b = __bfloat1622float2(xb[i]);
+        acc[t] = fmaf(a.x, b.x, acc[t]);
+        acc[t] = fmaf(a.y, b.y, acc[t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kFewMaxTokens; ++t) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+    if (lane == 0) part[warp][t] = acc[t];
+  }
+  __syncthreads();
+  if (threadIdx.x < p.T) {
+    float l = 0.0f;
+    for (int i = 0; i < kRouterThreads / 32; ++i) l += part[i][threadIdx.x];
+    if (p.bias) l += p.bias[e];
+    p.logits[threadIdx.x * p.E + e] = l;
+  }
+}
+
 // ------------------------------------------------------------- the schedule --
+
+// Quotients by a fixed divisor d: exact for n * d < 2^32.
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ explicit Div(int dd) : d((uint32_t)dd), m(dd > 1 ? 0xffffffffu / (uint32_t)dd + 1u : 0u) {}
+  __device__ __forceinline__ int quot(int n) const { return m ? (int)__umulhi((uint32_t)n, m) : n; }
+  __device__ __forceinline__ int rem(int n) const { return n - quot(n) * (int)d; }
+};
+
+// cp.async.bulk: `bytes` (a multiple of 16) from global to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 // The work of a CTA as a sequence of tiles, each a sequence of K slabs; the
 // producer and the consumers walk it alike.
@@ -449,10 +485,12 @@ struct GateUpWalk {
   int pos, end, u0, per;  // per: tiles of an expert
   __device__ __forceinline__ bool next(Tile& t) {
     if (pos >= end) return false;
-    t.u = u0 + pos / per;
-    t.r0 = pos % per * 8;
-    ++pos;
+    t = tile(pos++);
     return true;
+  }
+  __device__ __forceinline__ Tile tile(int at) const {
+    const int q = Div(per).quot(at);
+    return Tile{u0 + q, (at - q * per) * 8};
   }
 };
 
@@ -595,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* hfull = pempty + kWarps;     // an expert's rows of h are in shared memory
   uint64_t* hempty = hfull + kHRing;     // ... and have been used by all of its stages
   uint64_t* h_ready = hempty + kHRing;   // every CTA's h is written
-  uint64_t* x_done = h_ready + 1;        // x has been read for the last time
+  uint64_t* x_ready = h_ready + 1;       // x is in shared memory
+  uint64_t* x_done = x_ready + 1;        // ... and has been read for the last time
   uint64_t* turns = x_done + 1;          // an adding warp's turn to take sums
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
   volatile int* n_list = abort_flag + 1;
@@ -635,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&hempty[i], dr.tiles ? dr.tiles * i_slabs : 1);
     }
     mbar_init(h_ready, 1);
+    mbar_init(x_ready, 1);
     mbar_init(x_done, kWarps);
     for (int i = 0; i < kAcc; ++i) mbar_init(&turns[i], 1);
     *abort_flag = 0;
@@ -658,34 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   const int g = lane / 4, c = lane % 4;
-  // Activations into shared memory, in the operand layout, 8 inputs per thread and
-  // step. (x was complete before the router kernel passed its own wait.)
-  constexpr int kUnroll = 4;
-  const int per_row = H / 8, nvec = T * per_row;  // a multiple of 16 per row: whole half-warps
-  for (int v0 = threadIdx.x; v0 - lane < nvec; v0 += kUnroll * kConsumers) {
-    uint4 raws[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
-      if (v0 + i * kConsumers < nvec) raws[i] = __ldg(reinterpret_cast<const uint4*>(p.x) + v0 + i * kConsumers);
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int v = v0 + i * kConsumers;
-      if (v - lane >= nvec) break;
-      const bool live = v < nvec;
-      const uint4 raw = live ? raws[i] : make_uint4(0, 0, 0, 0);
-      const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 w2 = __bfloat1622float2(b[j]);
-        f[2 * j] = w2.x;
-        f[2 * j + 1] = w2.y;
-      }
-      store_operand<kW, true>(act + v / per_row * xpitch, L::scales_at(H), v % per_row, f, live);
-    }
+  pdl_wait();  // the logits, x in the operand layout, the cleared counter
+  if (threadIdx.x == kConsumers - 32) {  // (a warp without a token to select for)
+    mbar_arrive_expect_tx(x_ready, (uint32_t)(T * xpitch));
+    bulk_load(act, p.xrows, (uint32_t)(T * xpitch), x_ready);
   }
-
-  pdl_wait();  // the logits, the cleared counter
   if (warp < T) {
     // Top-k of token `warp`: order-preserving integer keys, ties to the lower
     // index, a NaN below everything; a taken expert's key is 0.
@@ -781,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles0 = walk0.end - walk0.pos;
   const int gu_tiles = tiles0 + walk1.end - walk1.pos, gu_stages = gu_tiles * h_slabs;
   const int per_entry = dr.tiles * i_slabs;  // stages of a list entry in the down phase
+  const Div by_h(h_slabs), by_i(i_slabs), by_entry(per_entry), by_expert(I / 8), by_rows(h_rows);
   const int all_stages = gu_stages + U * per_entry;
   bool ok = true;
 
@@ -804,27 +822,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* f;
       int kb;
       if (m < gu_stages) {
-        const int tile = m / h_slabs;
-        GateUpWalk w = tile < tiles0 ? walk0 : walk1;
-        w.pos += tile < tiles0 ? tile : tile - tiles0;
-        Tile t;
-        w.next(t);
-        const bool sh = S && t.u == 0;
-        kb = m % h_slabs * 8 + l;
+        const int tile = by_h.quot(m), at = tile < tiles0 ? walk0.pos + tile : walk1.pos + tile - tiles0;
+        const int q = by_expert.quot(at), r0 = 8 * (at - q * (I / 8));
+        const bool sh = tile < tiles0;
+        kb = (m - tile * h_slabs) * 8 + l;
         if (kb >= H / 128) return 0.0f;
         f = (lane < 8 ? (sh ? p.w.ss1 : p.w.s1) : (sh ? p.w.ss3 : p.w.s3)) +
-            ((int64_t)(sh ? 0 : list[t.u]) * (I / 128) + t.r0 / 128) * (H / 128);
+            ((int64_t)(sh ? 0 : list[S + q]) * (I / 128) + r0 / 128) * (H / 128);
       } else {
         m -= gu_stages;
-        const int u = down_entry(m / per_entry, U, S), tile = m % per_entry / i_slabs;
+        const int i = by_entry.quot(m), u = down_entry(i, U, S), tile = by_i.quot(m - i * per_entry);
         const bool sh = S && u == 0;
-        kb = m % i_slabs * 8 + l;
+        kb = (m - i * per_entry - tile * i_slabs) * 8 + l;
         if (kb >= I / 128) return 0.0f;
         const int row = dr.first(tile) + (lane < 8 ? 0 : dr.count(tile) - 1);
         f = (sh ? p.w.ss2 : p.w.s2) + ((int64_t)(sh ? 0 : list[u]) * (H / 128) + row / 128) * (I / 128);
       }
       return __ldg(f + kb);
     };
+    if (ok) ok = warp_wait<false>(x_ready, 0, p.status, abort_flag, 0x200d, 0, p.wait_ns);
     float next_scale = warp < A ? fetch_scale(warp) : 0.0f;
     bool x_used = true;
     for (int n = warp; n < all_stages && warp < A; n += A) {
@@ -841,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k0, row_bytes, entry = 0, sel0 = 0, sel1 = 8;
       Operands o;
       if (gate_up) {
-        k0 = n % h_slabs * F::kSlab;
+        k0 = by_h.rem(n) * F::kSlab;
         row_bytes = h_bytes;
         o.x = act + min(g, T - 1) * xpitch;  // lanes past the last token repeat it; their columns are not used
         o.s0 = reinterpret_cast<const float*>(act + min(2 * c, T - 1) * xpitch + L::scales_at(H));
@@ -849,9 +865,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.r0 = g * 128;
         o.step = 8 * 128;
       } else {
-        const int m = n - gu_stages, u = down_entry(m / per_entry, U, S), tile = m % per_entry / i_slabs;
-        entry = m / per_entry;
-        k0 = m % i_slabs * F::kSlab;
+        entry = by_entry.quot(n - gu_stages);
+        const int m = n - gu_stages - entry * per_entry, u = down_entry(entry, U, S), tile = by_i.quot(m);
+        k0 = (m - tile * i_slabs) * F::kSlab;
         row_bytes = i_bytes;
         if (ok)
           ok = warp_wait<false>(&hfull[entry % kHRing], (uint32_t)(entry / kHRing) & 1u, p.status, abort_flag, 0x2005, n,
@@ -859,10 +875,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Row of a token that uses the expert; the other columns repeat its first row and
         // are not used. (first[] is complete before any entry is.)
         const uint32_t mask = used[u];
-        const int row0 = ok ? first[entry] : 0;
+        const int row0 = ok ? by_rows.rem(first[entry]) : 0;
         auto row_of = [&](int tok) {
-          const int r = (mask >> tok) & 1u ? __popc(mask & ((1u << tok) - 1u)) : 0;
-          return act + (row0 + r) % h_rows * hpitch;
+          const int r = row0 + ((mask >> tok) & 1u ? __popc(mask & ((1u << tok) - 1u)) : 0);
+          return act + (r >= h_rows ? r - h_rows : r) * hpitch;
         };
         o.x = row_of(g);
         o.s0 = reinterpret_cast<const float*>(row_of(2 * c) + L::scales_at(I));
@@ -934,45 +950,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_bar_sync(4, kPrep * 32);
     if (ok) ok = warp_wait<false>(x_done, 0, p.status, abort_flag, 0x200a, 0, p.wait_ns);
     if (ok) ok = warp_wait<false>(h_ready, 0, p.status, abort_flag, 0x200b, 0, p.wait_ns);
-    int freed = 0;  // entries whose rows are free again
-    for (int i = 0; i < U; ++i) {
-      const int u = down_entry(i, U, S);
-      uint32_t mask = used[u];
-      const int end = first[i] + __popc(mask);
-      // (first[] counts on from entry to entry, so the oldest rows go first.)
-      while (ok && (freed <= i - kHRing || first[freed] < end - h_rows)) {
-        ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c, i,
-                              p.wait_ns);
-        ++freed;
+    // The four warps share each row, 128 groups of 8 values a pass and two passes a
+    // step; a step's values are fetched while the step before is stored.
+    struct Step {
+      int i, u, r, j;  // entry, its list index, row of the entry, first pass
+      uint32_t mask;   // the entry's tokens from this row on
+    };
+    const int groups = I / 8, mine = me * 32 + lane;
+    auto start = [&](int i) {
+      Step st{i, 0, 0, 0, 0u};
+      if (i < U) {
+        st.u = down_entry(i, U, S);
+        st.mask = used[st.u];
       }
-      for (int r = 0; mask; ++r, mask &= mask - 1) {
-        if ((first[i] + r) % kPrep != me) continue;
-        const float4* src =
-            reinterpret_cast<const float4*>(p.h + ((int64_t)u * kFewMaxTokens + __ffs(mask) - 1) * I);
-        uint8_t* row = act + (first[i] + r) % h_rows * hpitch;
-        constexpr int kBatch = 6;
-        for (int v0 = lane; v0 - lane < I / 8; v0 += 32 * kBatch) {
-          float4 raw[2 * kBatch];
+      return st;
+    };
+    auto after = [&](Step st) {
+      st.j += 2;
+      if (st.j * 128 < groups) return st;
+      st.j = 0;
+      ++st.r;
+      st.mask &= st.mask - 1;
+      return st.mask ? st : start(st.i + 1);
+    };
+    auto fetch = [&](const Step& st, float4 (&v)[4]) {
+      if (st.i >= U) return;
+      const float4* src = reinterpret_cast<const float4*>(p.h + ((int64_t)st.u * kFewMaxTokens + __ffs(st.mask) - 1) * I);
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            if (v0 + 32 * j >= I / 8) continue;
-            raw[2 * j] = __ldcg(src + 2 * (v0 + 32 * j));
-            raw[2 * j + 1] = __ldcg(src + 2 * (v0 + 32 * j) + 1);
-          }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int v = v0 + 32 * j;
-            if (v - lane >= I / 8) break;
-            const bool live = v < I / 8;
-            const float4 a = live ? raw[2 * j] : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 b = live ? raw[2 * j + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            store_operand<kW, false>(row, L::scales_at(I), v, f, live);
-          }
+      for (int j = 0; j < 2; ++j) {
+        const int g8 = (st.j + j) * 128 + mine;
+        v[2 * j] = g8 < groups ? __ldcg(src + 2 * g8) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[2 * j + 1] = g8 < groups ? __ldcg(src + 2 * g8 + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    int freed = 0;  // entries whose rows are free again
+    Step st = start(0);
+    float4 v[4];
+    fetch(st, v);
+    while (st.i < U) {
+      const Step nx = after(st);
+      float4 w[4];
+      fetch(nx, w);
+      if (st.r == 0 && st.j == 0) {
+        // Room for the entry's rows: first[] counts on from entry to entry, the oldest go first.
+        const int end = first[st.i] + __popc(st.mask);
+        while (ok && (freed <= st.i - kHRing || first[freed] < end - h_rows)) {
+          ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c,
+                                st.i, p.wait_ns);
+          ++freed;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&hfull[i % kHRing]);
+      uint8_t* row = act + by_rows.rem(first[st.i] + st.r) * hpitch;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int g8 = (st.j + j) * 128 + mine;
+        if (g8 - lane >= groups) break;
+        const float f[8] = {v[2 * j].x,     v[2 * j].y,     v[2 * j].z,     v[2 * j].w,
+                            v[2 * j + 1].x, v[2 * j + 1].y, v[2 * j + 1].z, v[2 * j + 1].w};
+        store_operand<kW, false>(row, L::scales_at(I), g8, f, g8 < groups);
+      }
+      if (nx.i != st.i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hfull[st.i % kHRing]);
+      }
+      st = nx;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = w[j];
     }
     return;
   }
@@ -1106,7 +1149,8 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
   const int smem = Smem<kW>::tile_offset(p.T, p.H, p.I, p.n_stages) + p.n_stages * kRows * Fmt<kW>::kSlab + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(few_router_kernel, dim3((unsigned)p.E), dim3(kRouterThreads), 0, s, 1, p);
+  const unsigned x_ctas = (unsigned)ceil_div((int64_t)p.T * p.H / 8, kRouterThreads);
+  e = launch_pdl(few_router_kernel<kW>, dim3((unsigned)p.E + x_ctas), dim3(kRouterThreads), 0, s, 1, p);
   if (e != cudaSuccess) return e;
   // Cooperative: the CTAs wait for one another, so all of them have to be resident.
   cudaLaunchConfig_t cfg = {};
@@ -1131,6 +1175,15 @@ bool fits(int T, int H, int I, int sms) {
 }
 
 }  // namespace
+
+int64_t few_x_bytes(int wdtype, int T, int H) {
+  switch (wdtype) {
+    case MOE_WDTYPE_BF16: return (int64_t)T * Smem<MOE_WDTYPE_BF16>::pitch(H);
+    case MOE_WDTYPE_FP8_E4M3: return (int64_t)T * Smem<MOE_WDTYPE_FP8_E4M3>::pitch(H);
+    case MOE_WDTYPE_NVFP4: return (int64_t)T * Smem<MOE_WDTYPE_NVFP4>::pitch(H);
+    default: return (int64_t)T * Smem<MOE_WDTYPE_MXFP4>::pitch(H);
+  }
+}
 
 bool few_fits(int wdtype, int T, int H, int I, int sms) {
   switch (wdtype) {

@@ -22,6 +22,7 @@ struct FewParams {
   int32_t* topk_idx;       // [T, k] or null
   float* topk_w;
   float* logits;           // [T, E]
+  uint8_t* xrows;          // x as the gate/up products read it
   float* h;                // [list entries, 8, I]
   int* counter;            // grid barrier
   int* status;
@@ -38,6 +39,7 @@ struct FewMaps {
 
 // Whether T tokens leave room for the weight ring in shared memory.
 bool few_fits(int wdtype, int T, int H, int I, int sms);
+int64_t few_x_bytes(int wdtype, int T, int H);  // of FewParams::xrows
 cudaError_t launch_few(const FewParams& p, const FewMaps& tm, int wdtype, int sms, cudaStream_t s);
 
 }  // namespace moe
