@@ -801,17 +801,27 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   const int per2 = cfg->wdtype == MOE_WDTYPE_BF16 ? 1 : cfg->wdtype == MOE_WDTYPE_FP8_E4M3 ? 2 : 4;
   const int block = cfg->wdtype == MOE_WDTYPE_NVFP4 ? 16 : 32;
   const uint64_t H = cfg->hidden, I = cfg->inter, E = cfg->n_experts;
+  const FewRows fr = few_rows(cfg->wdtype, cfg->hidden, sms);
+  p.cta_rows = fr.cta;
+  p.group_rows = fr.group;
+  p.down_lines = fr.lines;
+  const uint32_t gu_lines = per2 < 4 ? 8 : 4;
   auto one = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows, uint64_t K,
-                 uint32_t box_rows) {
-    const uint32_t lines = per2 < 4 ? 8 : 4;  // of a slab
+                 uint32_t box_rows, uint32_t lines) {
     return map_rows(code, cp, K * 2 / per2, rows, box_rows, lines) &&
            (per2 < 4 || map_u8(scale, sp, K / block, rows, lines * 256 / block, box_rows));
   };
-  bool ok = one(&tm.w1, &tm.s1, w->w1, w->s1, E * I, H, 8) && one(&tm.w3, &tm.s3, w->w3, w->s3, E * I, H, 8) &&
-            one(&tm.w2, &tm.s2, w->w2, w->s2, E * H, I, 4);
+  auto gu = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows) {
+    return one(code, scale, cp, sp, rows, H, 8, gu_lines);
+  };
+  auto down = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows) {
+    return one(code, scale, cp, sp, rows, I, (uint32_t)fr.group, (uint32_t)fr.lines);
+  };
+  bool ok = gu(&tm.w1, &tm.s1, w->w1, w->s1, E * I) && gu(&tm.w3, &tm.s3, w->w3, w->s3, E * I) &&
+            down(&tm.w2, &tm.s2, w->w2, w->s2, E * H);
   if (cfg->n_shared)
-    ok = ok && one(&tm.sw1, &tm.ss1, w->sw1, w->ss1, I, H, 8) && one(&tm.sw3, &tm.ss3, w->sw3, w->ss3, I, H, 8) &&
-         one(&tm.sw2, &tm.ss2, w->sw2, w->ss2, H, I, 4);
+    ok = ok && gu(&tm.sw1, &tm.ss1, w->sw1, w->ss1, I) && gu(&tm.sw3, &tm.ss3, w->sw3, w->ss3, I) &&
+         down(&tm.sw2, &tm.ss2, w->sw2, w->ss2, H);
   if (!ok) return MOE_ERR_CUDA;
   CUDA_TRY(launch_few(p, tm, cfg->wdtype, sms, reinterpret_cast<cudaStream_t>(stream)));
   return MOE_OK;

@@ -95,8 +95,8 @@ struct Smem {
   static constexpr int kUsed = kList + ((kMaxU * 4 + 15) / 16) * 16; // uint [kMaxU] token masks
   static constexpr int kFirst = kUsed + ((kMaxU * 4 + 15) / 16) * 16;  // int [kMaxU + 1] rows of h before an entry
   static constexpr int kGate = kFirst + ((kMaxU * 4 + 4 + 15) / 16) * 16;  // float [kMaxU][8]
-  static constexpr int kRed = kGate + kMaxU * kFewMaxTokens * 4;     // float [kWarps][32][4] partial sums
-  static constexpr int kDown = kRed + kWarps * 128 * 4;              // float [kFewDownTiles][32][4] output sums
+  static constexpr int kRed = kGate + kMaxU * kFewMaxTokens * 4;     // float [kWarps][2][32][4] partial sums
+  static constexpr int kDown = kRed + kWarps * 256 * 4;              // float [kFewDownTiles][32][4] output sums
   static constexpr int kX = kDown + kFewDownTiles * 128 * 4;
   static_assert(kX % 16 == 0, "alignment");
   // A row of K activations: operands, padding, block scales.
@@ -234,13 +234,14 @@ __device__ __forceinline__ void weigh(float (&acc)[4], const float (&d)[4], floa
   acc[3] = b.y;
 }
 
-// What a lane needs of a stage: the weight tile and its scale bytes, the offsets of
-// line 0 of its two rows (g, g + 8) and from line to line, the token's activations
-// (token g) and the block scales of the tokens of its columns (2c, 2c + 1).
+// What a lane needs of a stage: the weight tile and its scale bytes; the offsets of
+// line 0 of its two rows (g, g + 8 of an MMA tile) and from line to line, and of the
+// rows' scale bytes; the token's activations (token g) and the block scales of the
+// tokens of its columns (2c, 2c + 1).
 struct Operands {
   const uint8_t *tile, *scales, *x;
   const float *s0, *s1;
-  int r0, r1, step;
+  int r0, r1, step, c0, c1;
 };
 
 // acc += rows x tokens over line l of the stage, whose number in the whole row is kl.
@@ -248,7 +249,7 @@ struct Operands {
 template <int kW>
 __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, int kl, float sb0, float sb1, int lane) {
   using F = Fmt<kW>;
-  const int g = lane / 4, c = lane % 4;
+  const int c = lane % 4;
   const int o0 = o.r0 + l * o.step, o1 = o.r1 + l * o.step;
   // The 128-byte swizzle: 16-byte unit i of a line lies at i ^ (line address / 128 % 8).
   const int x0 = (o0 >> 7 & 7) << 4, x1 = (o1 >> 7 & 7) << 4;
@@ -256,8 +257,8 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, in
     // Eight 32-input blocks, two MMAs each (lane c takes the block's word c); a
     // block's sum is weighted by both scales.
     const uint8_t *a0 = o.tile + o0 + 4 * c, *a1 = o.tile + o1 + 4 * c;
-    const uint2 w0 = *reinterpret_cast<const uint2*>(o.scales + g * F::kScaleSlab + l * 8);
-    const uint2 w1 = *reinterpret_cast<const uint2*>(o.scales + (g + 8) * F::kScaleSlab + l * 8);
+    const uint2 w0 = *reinterpret_cast<const uint2*>(o.scales + o.c0 + l * 8);
+    const uint2 w1 = *reinterpret_cast<const uint2*>(o.scales + o.c1 + l * 8);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 s0 = reinterpret_cast<const float4*>(o.s0)[2 * kl + h];
@@ -304,8 +305,8 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, in
       } else {
         // NVFP4: the codes times their 16-input scale, exact in f16 (5 significant
         // bits, 2^-10 to 2688); 128 inputs a half, with one activation scale.
-        const uint32_t sa = *reinterpret_cast<const uint16_t*>(o.scales + g * F::kScaleSlab + l * 16 + h * 8 + 2 * c);
-        const uint32_t sb = *reinterpret_cast<const uint16_t*>(o.scales + (g + 8) * F::kScaleSlab + l * 16 + h * 8 + 2 * c);
+        const uint32_t sa = *reinterpret_cast<const uint16_t*>(o.scales + o.c0 + l * 16 + h * 8 + 2 * c);
+        const uint32_t sb = *reinterpret_cast<const uint16_t*>(o.scales + o.c1 + l * 16 + h * 8 + 2 * c);
         const uint32_t wa[2] = {f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x11))};
         const uint32_t wb[2] = {f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x11))};
         float e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -501,19 +502,24 @@ __device__ __forceinline__ GateUpWalk gate_up_walk(const FewParams& p, int u0, i
                     u0, per};
 }
 
-// Down: this CTA's output rows, a multiple of 4 of them, in tiles of up to 16; every
-// list entry in turn (the shared expert last), every tile of it.
+// Down: this CTA's output rows [r0, r0 + rows), in groups of p.group_rows (a multiple
+// of 4, at most 32: two 16-row MMA tiles); every list entry in turn (the shared expert
+// last), every group of it, every slab of p.down_lines lines.
 struct DownRows {
-  int r0, rows, tiles;
-  __device__ __forceinline__ int first(int tile) const { return r0 + 16 * tile; }
-  __device__ __forceinline__ int count(int tile) const { return min(16, rows - 16 * tile); }
+  int r0, rows, groups, per, slabs, lines;
+  __device__ __forceinline__ int first(int group) const { return r0 + per * group; }
+  __device__ __forceinline__ int count(int group) const { return min(per, rows - per * group); }
 };
 
-__device__ __forceinline__ DownRows down_rows(const FewParams& p) {
-  const int units = p.H / 4;
-  const int a = 4 * (int)((int64_t)units * blockIdx.x / gridDim.x);
-  const int b = 4 * (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
-  return DownRows{a, b - a, (b - a + 15) / 16};
+__device__ __forceinline__ DownRows down_rows(const FewParams& p, int row_lines) {
+  DownRows d;
+  d.r0 = (int)blockIdx.x * p.cta_rows;
+  d.rows = max(0, min(p.cta_rows, p.H - d.r0));
+  d.per = p.group_rows;
+  d.groups = (d.rows + d.per - 1) / d.per;
+  d.lines = p.down_lines;
+  d.slabs = (row_lines + d.lines - 1) / d.lines;
+  return d;
 }
 
 // List entry of step i of the down phase.
@@ -540,34 +546,29 @@ struct Producer {
   uint32_t issued = 0, issued_phase = 0;  // per slot: loaded at all, and the phase of the last load
 };
 
-// Loads the K slabs of a tile: `boxes` boxes of kBoxRows rows from row0 (with two
-// maps, the same rows of each: gate and up). One thread, and as few instructions per
+// Loads the K slabs of a tile: boxes of `rows` rows from row0 and slab_bytes of each
+// (with two maps, the same rows of both: gate and up). One thread, and as few instructions per
 // stage as possible: at the HBM rate a stage takes about 700 clocks, and a TMA
 // instruction costs its thread more than 100.
-template <int kW, bool kScales, int kBoxRows, bool kTwoMaps>
-__device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>& pr, int boxes, const CUtensorMap* m0,
-                                          const CUtensorMap* m1, int row0, int slabs, volatile int* abort_flag) {
+template <int kW, bool kScales, bool kTwoMaps>
+__device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>& pr, const CUtensorMap* m0,
+                                          const CUtensorMap* m1, int row0, int rows, int slab_bytes, int slabs,
+                                          volatile int* abort_flag) {
   using F = Fmt<kW>;
-  constexpr int kBytes = kScales ? F::kScaleSlab : F::kSlab;  // of a row
-  const uint32_t bytes = (uint32_t)(boxes * kBoxRows * kBytes);
+  constexpr int kSlot = kRows * (kScales ? F::kScaleSlab : F::kSlab);
+  const uint32_t bytes = (uint32_t)((kTwoMaps ? 2 : 1) * rows * slab_bytes);
   for (int k = 0; k < slabs; ++k) {
     const int st = pr.rg.stage;
     if (!mbar_wait(&pr.empty[st], pr.rg.phase ^ 1u, p.status, abort_flag, 0x2001, k, p.wait_ns)) return false;
     uint64_t* bar = &pr.full[st];
     mbar_arrive_expect_tx(bar, bytes);
-    uint8_t* dst = pr.dst + st * (kRows * kBytes);
-    auto load = [&](uint8_t* to, const CUtensorMap* m, int row) {
-      if constexpr (kScales) tma_load_2d(to, m, bar, k * kBytes, row);
-      else tma_load_rows(to, m, bar, row, k * (kBytes / 128));
+    uint8_t* dst = pr.dst + st * kSlot;
+    auto load = [&](uint8_t* to, const CUtensorMap* m) {
+      if constexpr (kScales) tma_load_2d(to, m, bar, k * slab_bytes, row0);
+      else tma_load_rows(to, m, bar, row0, k * (slab_bytes / 128));
     };
-    if constexpr (kTwoMaps) {
-      load(dst, m0, row0);
-      load(dst + kBoxRows * kBytes, m1, row0);
-    } else {
-#pragma unroll
-      for (int b = 0; b < kRows / kBoxRows; ++b)
-        if (b < boxes) load(dst + b * kBoxRows * kBytes, m0, row0 + b * kBoxRows);
-    }
+    load(dst, m0);
+    if (kTwoMaps) load(dst + rows * slab_bytes, m1);
     pr.issued |= 1u << st;
     pr.issued_phase ^= ((pr.issued_phase >> st ^ pr.rg.phase) & 1u) << st;
     pr.rg.step(pr.n_stages);
@@ -579,7 +580,7 @@ __device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>&
 template <int kW, bool kScales>
 __device__ __forceinline__ void produce(const FewParams& p, const FewMaps& tm, uint8_t* dst, uint64_t* full,
                                         uint64_t* empty, const int* list, volatile int* n_list, volatile int* abort_flag,
-                                        int h_slabs, int i_slabs, int lane) {
+                                        int h_slabs, const DownRows& dr, int lane) {
   Producer<kScales> pr{dst, full, empty, p.n_stages};
   bool ok = p.inject != 1;
   const CUtensorMap *g = kScales ? &tm.s1 : &tm.w1, *u = kScales ? &tm.s3 : &tm.w3, *d = kScales ? &tm.s2 : &tm.w2;
@@ -589,8 +590,8 @@ __device__ __forceinline__ void produce(const FewParams& p, const FewMaps& tm, u
     Tile t;
     while (ok && w.next(t)) {
       const bool sh = p.S && t.u == 0;
-      ok = load_tile<kW, kScales, 8, true>(p, pr, 2, sh ? sg : g, sh ? su : u, (sh ? 0 : list[t.u]) * p.I + t.r0, h_slabs,
-                                           abort_flag);
+      ok = load_tile<kW, kScales, true>(p, pr, sh ? sg : g, sh ? su : u, (sh ? 0 : list[t.u]) * p.I + t.r0, 8,
+                                        kScales ? Fmt<kW>::kScaleSlab : Fmt<kW>::kSlab, h_slabs, abort_flag);
     }
   };
   if (lane == 0) gate_up(gate_up_walk(p, 0, p.S));  // the shared expert: needs no routing
@@ -599,14 +600,14 @@ __device__ __forceinline__ void produce(const FewParams& p, const FewMaps& tm, u
   if (lane != 0) return;
   const int U = *n_list;
   gate_up(gate_up_walk(p, p.S, U - p.S));
-  const DownRows dr = down_rows(p);
+  const int slab_bytes = dr.lines * (kScales ? Fmt<kW>::kScaleSlab / (Fmt<kW>::kSlab / kLine) : kLine);
   for (int i = 0; i < U && ok; ++i) {
     const int e = down_entry(i, U, p.S);
     const bool sh = p.S && e == 0;
     const int base = (sh ? 0 : list[e]) * p.H;
-    for (int tile = 0; tile < dr.tiles && ok; ++tile)
-      ok = load_tile<kW, kScales, 4, false>(p, pr, dr.count(tile) / 4, sh ? sd : d, nullptr, base + dr.first(tile),
-                                            i_slabs, abort_flag);
+    for (int q = 0; q < dr.groups && ok; ++q)
+      ok = load_tile<kW, kScales, false>(p, pr, sh ? sd : d, nullptr, base + dr.first(q), dr.per, slab_bytes, dr.slabs,
+                                         abort_flag);
   }
   // Let every copy land before the thread leaves (the others wait for them too, unless a wait gave up).
   for (int s = 0; s < p.n_stages; ++s) {
@@ -655,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* scales = smem + L::scale_offset(T, H, I);
   uint8_t* tiles = smem + L::tile_offset(T, H, I, n_stages);
   const int h_bytes = H * 2 / F::kPer2, i_bytes = I * 2 / F::kPer2;  // bytes of a W1/W3 and a W2 row
-  const int h_slabs = (h_bytes + F::kSlab - 1) / F::kSlab, i_slabs = (i_bytes + F::kSlab - 1) / F::kSlab;
+  const int h_slabs = (h_bytes + F::kSlab - 1) / F::kSlab;
   const int xpitch = L::pitch(H), hpitch = L::pitch(I);
   const int h_rows = L::act_bytes(T, H, I) / hpitch;  // rows of h that the activations' space holds, T at least
-  const DownRows dr = down_rows(p);
+  const DownRows dr = down_rows(p, i_bytes / kLine);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < n_stages; ++i) {
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kHRing; ++i) {
       mbar_init(&hfull[i], kPrep);
-      mbar_init(&hempty[i], dr.tiles ? dr.tiles * i_slabs : 1);
+      mbar_init(&hempty[i], dr.rows ? dr.groups * dr.slabs : 1);
     }
     mbar_init(h_ready, 1);
     mbar_init(x_ready, 1);
@@ -686,12 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   if (warp == kWarps + kAcc + kPrep) {
-    produce<kW, false>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, i_slabs, lane);
+    produce<kW, false>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
     return;
   }
   if (warp == kWarps + kAcc + kPrep + 1) {
     if constexpr (kScaleBytes)
-      produce<kW, true>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, i_slabs, lane);
+      produce<kW, true>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
     else
       named_bar_arrive(1, kThreads);
     return;
@@ -797,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const GateUpWalk walk0 = gate_up_walk(p, 0, S), walk1 = gate_up_walk(p, S, U - S);
   const int tiles0 = walk0.end - walk0.pos;
   const int gu_tiles = tiles0 + walk1.end - walk1.pos, gu_stages = gu_tiles * h_slabs;
-  const int per_entry = dr.tiles * i_slabs;  // stages of a list entry in the down phase
-  const Div by_h(h_slabs), by_i(i_slabs), by_entry(per_entry), by_expert(I / 8), by_rows(h_rows);
+  const int per_entry = dr.groups * dr.slabs;  // stages of a list entry in the down phase
+  const Div by_h(h_slabs), by_i(dr.slabs), by_entry(per_entry), by_expert(I / 8), by_rows(h_rows);
   const int all_stages = gu_stages + U * per_entry;
   bool ok = true;
 
@@ -831,11 +832,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ((int64_t)(sh ? 0 : list[S + q]) * (I / 128) + r0 / 128) * (H / 128);
       } else {
         m -= gu_stages;
-        const int i = by_entry.quot(m), u = down_entry(i, U, S), tile = by_i.quot(m - i * per_entry);
+        const int i = by_entry.quot(m), u = down_entry(i, U, S), q = by_i.quot(m - i * per_entry);
         const bool sh = S && u == 0;
-        kb = (m - i * per_entry - tile * i_slabs) * 8 + l;
-        if (kb >= I / 128) return 0.0f;
-        const int row = dr.first(tile) + (lane < 8 ? 0 : dr.count(tile) - 1);
+        kb = (m - i * per_entry - q * dr.slabs) * dr.lines + l;
+        if (l >= dr.lines || kb >= I / 128) return 0.0f;
+        const int row = dr.first(q) + (lane < 8 ? 0 : dr.count(q) - 1);
         f = (sh ? p.w.ss2 : p.w.s2) + ((int64_t)(sh ? 0 : list[u]) * (H / 128) + row / 128) * (I / 128);
       }
       return __ldg(f + kb);
@@ -852,23 +853,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(x_done);
         x_used = false;
       }
-      // The stage's K range, the token rows, and where the weight rows lie: in boxes
-      // of eight rows, or of four.
-      int k0, row_bytes, entry = 0, sel0 = 0, sel1 = 8;
+      // The stage's lines, the token rows, and where the weight rows lie: line after line
+      // of eight gate rows, and the same of the up rows behind them; or of a group's rows.
+      int kl0, lines, entry = 0, group = 0;
       Operands o;
       if (gate_up) {
-        k0 = by_h.rem(n) * F::kSlab;
-        row_bytes = h_bytes;
+        kl0 = by_h.rem(n) * (F::kSlab / kLine);
+        lines = min(F::kSlab / kLine, h_bytes / kLine - kl0);
         o.x = act + min(g, T - 1) * xpitch;  // lanes past the last token repeat it; their columns are not used
         o.s0 = reinterpret_cast<const float*>(act + min(2 * c, T - 1) * xpitch + L::scales_at(H));
         o.s1 = reinterpret_cast<const float*>(act + min(2 * c + 1, T - 1) * xpitch + L::scales_at(H));
-        o.r0 = g * 128;
-        o.step = 8 * 128;
       } else {
         entry = by_entry.quot(n - gu_stages);
-        const int m = n - gu_stages - entry * per_entry, u = down_entry(entry, U, S), tile = by_i.quot(m);
-        k0 = (m - tile * i_slabs) * F::kSlab;
-        row_bytes = i_bytes;
+        const int m = n - gu_stages - entry * per_entry, u = down_entry(entry, U, S);
+        group = by_i.quot(m);
+        kl0 = (m - group * dr.slabs) * dr.lines;
+        lines = min(dr.lines, i_bytes / kLine - kl0);
         if (ok)
           ok = warp_wait<false>(&hfull[entry % kHRing], (uint32_t)(entry / kHRing) & 1u, p.status, abort_flag, 0x2005, n,
                                 p.wait_ns);
@@ -883,18 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.x = row_of(g);
         o.s0 = reinterpret_cast<const float*>(row_of(2 * c) + L::scales_at(I));
         o.s1 = reinterpret_cast<const float*>(row_of(2 * c + 1) + L::scales_at(I));
-        o.r0 = (g / 4) * 4 * F::kSlab + (g % 4) * 128;
-        o.step = 4 * 128;
-        if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-          const int top = dr.first(tile) / 128;
-          sel0 = (dr.first(tile) + g) / 128 != top ? 8 : 0;
-          sel1 = (dr.first(tile) + g + 8) / 128 != top ? 8 : 0;
-        }
       }
-      o.r1 = o.r0 + 8 * F::kSlab;
-      const int lines = min(F::kSlab, row_bytes - k0) / kLine, kl0 = k0 / kLine;
-      Sums acc;
-      acc.clear();
       // Stage n's slot held stage n - n_stages before, which another warp may not even
       // have seen land: its release is waited for first, or the parity of `full` could
       // be taken for the phase before. (The release before that one is certain: stage
@@ -902,18 +891,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A <= n_stages.)
       if (ok) ok = warp_wait<false>(&empty[rg.stage], rg.phase ^ 1u, p.status, abort_flag, 0x2007, n, p.wait_ns);
       if (ok) ok = warp_wait<false>(&full[rg.stage], rg.phase, p.status, abort_flag, 0x2002, n, p.wait_ns);
-      if (ok) {
-        o.tile = tiles + rg.stage * (kRows * F::kSlab);
-        o.scales = scales + rg.stage * L::kStageScales;
-#pragma unroll(kW == MOE_WDTYPE_BF16 || kW == MOE_WDTYPE_FP8_E4M3 ? 2 : 1)
-        for (int l = 0; l < lines; ++l) {
-          float sb0 = 1.0f, sb1 = 1.0f;
+      o.tile = tiles + rg.stage * (kRows * F::kSlab);
+      o.scales = scales + rg.stage * L::kStageScales;
+      // Gate/up: one tile of 8 + 8 rows; down: one or two of 16 rows of the group.
+      const int parts = gate_up ? 1 : (dr.count(group) + 15) / 16;
+      float4 sums[2];
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part >= parts) break;
+        int sel0 = 0, sel1 = 8;
+        if (gate_up) {
+          o.r0 = g * 128;
+          o.r1 = o.r0 + 8 * F::kSlab;
+          o.step = 8 * 128;
+          o.c0 = g * F::kScaleSlab;
+          o.c1 = (g + 8) * F::kScaleSlab;
+        } else {
+          // (Rows past the group repeat its last one; their sums are not used.)
+          const int a = min(16 * part + g, dr.per - 1), b = min(16 * part + g + 8, dr.per - 1);
+          o.r0 = a * 128;
+          o.r1 = b * 128;
+          o.step = dr.per * 128;
+          o.c0 = a * (dr.lines * F::kScaleSlab / (F::kSlab / kLine));
+          o.c1 = b * (dr.lines * F::kScaleSlab / (F::kSlab / kLine));
           if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-            sb0 = __shfl_sync(0xffffffffu, scale, sel0 + l);
-            sb1 = __shfl_sync(0xffffffffu, scale, sel1 + l);
+            const int top = dr.first(group) / 128;
+            sel0 = (dr.first(group) + a) / 128 != top ? 8 : 0;
+            sel1 = (dr.first(group) + b) / 128 != top ? 8 : 0;
           }
-          line_mma<kW>(acc, o, l, kl0 + l, sb0, sb1, lane);
         }
+        Sums acc;
+        acc.clear();
+        if (ok) {
+#pragma unroll(kW == MOE_WDTYPE_BF16 || kW == MOE_WDTYPE_FP8_E4M3 ? 2 : 1)
+          for (int l = 0; l < lines; ++l) {
+            float sb0 = 1.0f, sb1 = 1.0f;
+            if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
+              sb0 = __shfl_sync(0xffffffffu, scale, sel0 + l);
+              sb1 = __shfl_sync(0xffffffffu, scale, sel1 + l);
+            }
+            line_mma<kW>(acc, o, l, kl0 + l, sb0, sb1, lane);
+          }
+        }
+        sums[part] = acc.total();
       }
       __syncwarp();
       if (lane == 0) {
@@ -922,7 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       advance(A);
       if (ok) ok = warp_wait<false>(&pempty[warp], pr.phase ^ 1u, p.status, abort_flag, 0x2004, n, p.wait_ns);
-      *reinterpret_cast<float4*>(red + warp * 128 + lane * 4) = acc.total();
+      *reinterpret_cast<float4*>(red + warp * 256 + lane * 4) = sums[0];
+      if (parts > 1) *reinterpret_cast<float4*>(red + warp * 256 + 128 + lane * 4) = sums[1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&pfull[warp]);
       pr.phase ^= 1u;
@@ -939,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The rows of a list entry's tokens lie one after another in the activations'
     // space, entries following entries around it (first[] counts the rows).
     const int me = warp - kWarps - kAcc;
-    if (dr.tiles == 0) return;  // no rows of the output here
+    if (dr.rows == 0) return;  // no rows of the output here
     if (me == 0 && lane == 0) {
       int rows = 0;
       for (int i = 0; i < U; ++i) {
@@ -1027,14 +1048,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int me = warp - kWarps;
   int n = 0, turn = 0;
   uint32_t turn_phase = 0;
-  auto take = [&](float (&s)[4]) {  // stage n's partial sums
-    const int w = n % A;
-    if (ok) ok = warp_wait<false>(&pfull[w], (uint32_t)(n / A) & 1u, p.status, abort_flag, 0x2006, n, p.wait_ns);
-    const float4 v = *reinterpret_cast<const float4*>(red + w * 128 + lane * 4);
-    s[0] += v.x;
-    s[1] += v.y;
-    s[2] += v.z;
-    s[3] += v.w;
+  const Div by_a(A);
+  auto take = [&](float (&s)[2][4], int parts) {  // stage n's partial sums
+    const int round = by_a.quot(n), w = n - round * A;
+    if (ok) ok = warp_wait<false>(&pfull[w], (uint32_t)round & 1u, p.status, abort_flag, 0x2006, n, p.wait_ns);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i >= parts) break;
+      const float4 v = *reinterpret_cast<const float4*>(red + w * 256 + i * 128 + lane * 4);
+      s[i][0] += v.x;
+      s[i][1] += v.y;
+      s[i][2] += v.z;
+      s[i][3] += v.w;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&pempty[w]);
     ++n;
@@ -1058,9 +1084,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       begin_turn();
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < h_slabs; ++k) take(s);
+      float both[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int k = 0; k < h_slabs; ++k) take(both, 1);
       end_turn();
+      float(&s)[4] = both[0];
       if constexpr (kW == MOE_WDTYPE_NVFP4) {
         const bool sh = S && t.u == 0;
         const int e = sh ? 0 : list[t.u];
@@ -1106,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // from it, whatever its weights hold.
   if (me != turn % kAcc) return;
   begin_turn();
-  for (int i = lane; i < dr.tiles * 128; i += 32) down[i] = 0.0f;
+  for (int i = lane; i < dr.groups * 256; i += 32) down[i] = 0.0f;
   __syncwarp();
   for (int i = 0; i < U; ++i) {
     const int u = down_entry(i, U, S);
@@ -1114,30 +1141,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     float s = 1.0f;
     if constexpr (kW == MOE_WDTYPE_NVFP4) s = (S && u == 0) ? p.w.sg2[0] : p.w.g2[list[u]];
     const float g0 = s * gates[u * kFewMaxTokens + 2 * c], g1 = s * gates[u * kFewMaxTokens + 2 * c + 1];
-    for (int tile = 0; tile < dr.tiles; ++tile) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < i_slabs; ++k) take(d);
-      float4* at = reinterpret_cast<float4*>(down + tile * 128 + lane * 4);
-      float4 acc = *at;
-      if ((mask >> (2 * c)) & 1u) {
-        acc.x = fmaf(d[0], g0, acc.x);
-        acc.z = fmaf(d[2], g0, acc.z);
+    for (int q = 0; q < dr.groups; ++q) {
+      const int parts = (dr.count(q) + 15) / 16;
+      float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int k = 0; k < dr.slabs; ++k) take(d, parts);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part >= parts) break;
+        float4* at = reinterpret_cast<float4*>(down + (2 * q + part) * 128 + lane * 4);
+        float4 acc = *at;
+        if ((mask >> (2 * c)) & 1u) {
+          acc.x = fmaf(d[part][0], g0, acc.x);
+          acc.z = fmaf(d[part][2], g0, acc.z);
+        }
+        if ((mask >> (2 * c + 1)) & 1u) {
+          acc.y = fmaf(d[part][1], g1, acc.y);
+          acc.w = fmaf(d[part][3], g1, acc.w);
+        }
+        *at = acc;
       }
-      if ((mask >> (2 * c + 1)) & 1u) {
-        acc.y = fmaf(d[1], g1, acc.y);
-        acc.w = fmaf(d[3], g1, acc.w);
-      }
-      *at = acc;
     }
   }
   if (!ok || *abort_flag) return;
-  for (int tile = 0; tile < dr.tiles; ++tile) {
-    const float4 acc = *reinterpret_cast<const float4*>(down + tile * 128 + lane * 4);
-    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+  for (int q = 0; q < dr.groups; ++q) {
+    for (int part = 0; 16 * part < dr.count(q); ++part) {
+      const float4 acc = *reinterpret_cast<const float4*>(down + (2 * q + part) * 128 + lane * 4);
+      const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = g + 8 * (j / 2), tok = 2 * c + j % 2;
-      if (r < dr.count(tile) && tok < T) p.out[(int64_t)tok * H + dr.first(tile) + r] = __float2bfloat16_rn(v[j]);
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * part + g + 8 * (j / 2), tok = 2 * c + j % 2;
+        if (r < dr.count(q) && tok < T) p.out[(int64_t)tok * H + dr.first(q) + r] = __float2bfloat16_rn(v[j]);
+      }
     }
   }
 }
@@ -1170,8 +1204,9 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
 
 template <int kW>
 bool fits(int T, int H, int I, int sms) {
-  // A ring of some stages, and the output sums of a CTA's rows.
-  return Smem<kW>::stages(T, H, I) >= 3 && ceil_div(ceil_div(H / 4, sms) * 4, 16) <= kFewDownTiles;
+  // A ring of some stages, and room for the output sums of a CTA's rows.
+  const FewRows r = few_rows(kW, H, sms);
+  return Smem<kW>::stages(T, H, I) >= 3 && 2 * ceil_div(r.cta, r.group) <= kFewDownTiles;
 }
 
 }  // namespace

@@ -9,11 +9,12 @@ namespace moe {
 
 constexpr int kFewMaxTokens = MOE_FEW_MAX_TOKENS;
 constexpr int kFewSmem = 227 * 1024;  // shared memory of a CTA
-constexpr int kFewDownTiles = 16;     // 16-row tiles of the output that a CTA may own
+constexpr int kFewDownTiles = 16;     // 16-row tiles of the output that a CTA may own (in pairs)
 
 struct FewParams {
   int32_t T, H, I, E, k, S;
   int32_t n_stages;        // weight ring (set by the launcher)
+  int32_t cta_rows, group_rows, down_lines;  // see FewRows
   const uint16_t* x;       // [T, H] bf16
   const uint16_t* router_w;
   const float* bias;       // [E] or null
@@ -30,9 +31,27 @@ struct FewParams {
   int32_t inject;
 };
 
-// Weight tensor maps: rows as [128 bytes, rows, lines], boxes of 128 bytes x 8 rows
-// (w1, w3) or 4 rows (w2) x a slab's 8 (BF16, FP8) or 4 lines, 128B-swizzled; 4-bit
-// storage: scale bytes [rows, K / block] in boxes of the same rows x a slab's scales.
+// Output rows of a CTA (a multiple of 4), the rows of them that a stage holds (as
+// even a split as fits 32), and lines of 128 bytes of each (a stage is 16 KB, or 8 KB
+// for 4-bit storage; MXFP4's 8 scale bytes of a line need a second line to make 16).
+struct FewRows {
+  int cta, group, lines;
+};
+inline FewRows few_rows(int wdtype, int H, int sms) {
+  FewRows r;
+  r.cta = (int)ceil_div(H / 4, sms) * 4;
+  const int groups = (int)ceil_div(r.cta, 32);
+  r.group = (int)ceil_div(r.cta / 4, groups) * 4;
+  const bool four = wdtype == MOE_WDTYPE_NVFP4 || wdtype == MOE_WDTYPE_MXFP4;
+  r.lines = (four ? 8192 : 16384) / (r.group * 128);
+  if (r.lines > (four ? 4 : 8)) r.lines = four ? 4 : 8;
+  if (wdtype == MOE_WDTYPE_MXFP4) r.lines &= ~1;
+  return r;
+}
+
+// Weight tensor maps: rows as [128 bytes, rows, lines], 128B-swizzled boxes of 8 rows
+// x 8 (BF16, FP8) or 4 lines (w1, w3), or as FewRows says (w2); 4-bit storage: scale
+// bytes [rows, K / block] in boxes of the same rows and inputs.
 struct FewMaps {
   CUtensorMap w1, w3, w2, sw1, sw3, sw2, s1, s3, s2, ss1, ss3, ss2;
 };
