@@ -805,7 +805,7 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.cta_rows = fr.cta;
   p.group_rows = fr.group;
   p.down_lines = fr.lines;
-  const uint32_t gu_lines = per2 < 4 ? 8 : 4;
+  constexpr uint32_t gu_lines = 8;
   auto one = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows, uint64_t K,
                  uint32_t box_rows, uint32_t lines) {
     return map_rows(code, cp, K * 2 / per2, rows, box_rows, lines) &&

@@ -43,50 +43,54 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;                    // multiplying warps
 constexpr int kAcc = 2;                      // warps that add up
 constexpr int kPrep = 4;                     // warps that bring h
-constexpr int kConsumers = (kWarps + kAcc + kPrep) * 32;
-constexpr int kThreads = kConsumers + 64;    // + the two producer warps
-constexpr int kHRing = 16;                   // experts of h in shared memory at most (more than kWarps)
+constexpr int kTeam = 1;                     // multiplying warps that share a stage
+constexpr int kHRing = 24;                   // experts of h in shared memory at most
 constexpr int kRows = 16;                    // rows of a stage
 constexpr int kLine = 128;                   // bytes of a row that a step multiplies
 constexpr int kMaxRing = 24;
 constexpr int kMaxU = kFewMaxTokens * kMaxTopK + 1;
-constexpr int kRouterThreads = 128;
+constexpr int kRouterThreads = 256;
+constexpr int kRouterExperts = 2;            // experts of a router CTA
 
 // Per storage: inputs per 2 bytes of a weight row, bytes of a row in a stage (a
 // slab), scale bytes per row and slab (4-bit storage), padding of an activation row in shared memory that keeps the
-// fragment loads free of bank conflicts, and inputs per activation block that
-// has a scale (0: activations stay bf16).
+// fragment loads free of bank conflicts, inputs per activation block that has
+// a scale (0: activations stay bf16), and multiplying warps.
 template <int kW>
 struct Fmt;
 template <>
 struct Fmt<MOE_WDTYPE_BF16> {
-  static constexpr int kPer2 = 1, kSlab = 1024, kScaleSlab = 0, kXPad = 64, kBlock = 0;
+  static constexpr int kPer2 = 1, kSlab = 1024, kScaleSlab = 0, kXPad = 64, kBlock = 0, kWarps = 8;
 };
 template <>
 struct Fmt<MOE_WDTYPE_FP8_E4M3> {
-  static constexpr int kPer2 = 2, kSlab = 1024, kScaleSlab = 0, kXPad = 16, kBlock = 128;
+  static constexpr int kPer2 = 2, kSlab = 1024, kScaleSlab = 0, kXPad = 16, kBlock = 128, kWarps = 8;
 };
 template <>
 struct Fmt<MOE_WDTYPE_NVFP4> {
-  static constexpr int kPer2 = 4, kSlab = 512, kScaleSlab = kSlab / 8, kXPad = 64, kBlock = 128;
+  static constexpr int kPer2 = 4, kSlab = 1024, kScaleSlab = kSlab / 8, kXPad = 64, kBlock = 128, kWarps = 8;
 };
 template <>
 struct Fmt<MOE_WDTYPE_MXFP4> {
-  static constexpr int kPer2 = 4, kSlab = 512, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 32;
+  static constexpr int kPer2 = 4, kSlab = 1024, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 32, kWarps = 8;
 };
 
 template <int kW>
 struct Smem {
   using F = Fmt<kW>;
+  static constexpr int kWarps = F::kWarps, kTeams = kWarps / kTeam;
+  static constexpr int kProducers = F::kScaleSlab ? 2 : 1;  // weight rows, scale bytes
+  static constexpr int kConsumers = (kWarps + kAcc + kPrep) * 32;
+  static constexpr int kThreads = kConsumers + kProducers * 32;
+  static_assert(kTeams < kHRing, "a team's stages must not skip a whole ring of experts");
   static constexpr int kStageScales = kRows * F::kScaleSlab;  // a stage's scale bytes
   static constexpr int kStage = kRows * F::kSlab + kStageScales;
   // Fixed part: barriers, tables, partial sums. Then the activations (x, later rows
   // of h), the scale bytes and the weight tiles.
   static constexpr int kBars = 0;
-  static constexpr int kNumBars = 2 * kMaxRing + 2 * kWarps + 2 * kHRing + 3 + kAcc;
+  static constexpr int kNumBars = 2 * kMaxRing + 2 * kTeams + 2 * kHRing + 3 + kAcc;
   static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;  // abort flag, list length
   static constexpr int kTopIdx = kMisc + 64;                         // int [8][16]
   static constexpr int kTopW = kTopIdx + kFewMaxTokens * kMaxTopK * 4;
@@ -234,66 +238,79 @@ __device__ __forceinline__ void weigh(float (&acc)[4], const float (&d)[4], floa
   acc[3] = b.y;
 }
 
-// What a lane needs of a stage: the weight tile and its scale bytes; the offsets of
-// line 0 of its two rows (g, g + 8 of an MMA tile) and from line to line, and of the
-// rows' scale bytes; the token's activations (token g) and the block scales of the
-// tokens of its columns (2c, 2c + 1).
+// Shared-memory loads by 32-bit address: through generic pointers every one of them
+// would carry 64-bit address arithmetic.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// What a lane needs of a line of a stage, as shared-memory addresses: its two weight
+// rows (g, g + 8 of an MMA tile) and their scale bytes, the token's activations (token
+// g) and the block scales of the tokens of its columns (2c, 2c + 1).
 struct Operands {
-  const uint8_t *tile, *scales, *x;
-  const float *s0, *s1;
-  int r0, r1, step, c0, c1;
+  uint32_t a0, a1, c0, c1, x, s0, s1;
 };
 
-// acc += rows x tokens over line l of the stage, whose number in the whole row is kl.
-// sb0, sb1 (FP8): weight scales of rows g and g + 8 in this line's 128 inputs.
+// acc += rows x tokens over a line. sb0, sb1 (FP8): weight scales of rows g and g + 8
+// in this line's 128 inputs.
 template <int kW>
-__device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, int kl, float sb0, float sb1, int lane) {
-  using F = Fmt<kW>;
+__device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0, float sb1, int lane) {
   const int c = lane % 4;
-  const int o0 = o.r0 + l * o.step, o1 = o.r1 + l * o.step;
   // The 128-byte swizzle: 16-byte unit i of a line lies at i ^ (line address / 128 % 8).
-  const int x0 = (o0 >> 7 & 7) << 4, x1 = (o1 >> 7 & 7) << 4;
+  const uint32_t x0 = (o.a0 >> 3) & 0x70u, x1 = (o.a1 >> 3) & 0x70u;
   if constexpr (kW == MOE_WDTYPE_MXFP4) {
     // Eight 32-input blocks, two MMAs each (lane c takes the block's word c); a
     // block's sum is weighted by both scales.
-    const uint8_t *a0 = o.tile + o0 + 4 * c, *a1 = o.tile + o1 + 4 * c;
-    const uint2 w0 = *reinterpret_cast<const uint2*>(o.scales + o.c0 + l * 8);
-    const uint2 w1 = *reinterpret_cast<const uint2*>(o.scales + o.c1 + l * 8);
+    const uint32_t a0 = o.a0 + 4 * c, a1 = o.a1 + 4 * c;
+    const uint2 w0 = lds64(o.c0), w1 = lds64(o.c1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float4 s0 = reinterpret_cast<const float4*>(o.s0)[2 * kl + h];
-      const float4 s1 = reinterpret_cast<const float4*>(o.s1)[2 * kl + h];
-      const float sx0[4] = {s0.x, s0.y, s0.z, s0.w}, sx1[4] = {s1.x, s1.y, s1.z, s1.w};
+      const uint4 s0 = lds128(o.s0 + 16 * h), s1 = lds128(o.s1 + 16 * h);
+      const uint32_t sx0[4] = {s0.x, s0.y, s0.z, s0.w}, sx1[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int u = (4 * h + b) << 4;
+        const uint32_t u = (uint32_t)(4 * h + b) << 4;
         uint32_t va[4], vb[4];
-        f16_of_e2m1x8(*reinterpret_cast<const uint32_t*>(a0 + (u ^ x0)), va);
-        f16_of_e2m1x8(*reinterpret_cast<const uint32_t*>(a1 + (u ^ x1)), vb);
-        const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 512 + (4 * h + b) * 64 + 16 * c);
+        f16_of_e2m1x8(lds32(a0 + (u ^ x0)), va);
+        f16_of_e2m1x8(lds32(a1 + (u ^ x1)), vb);
+        const uint4 x = lds128(o.x + (4 * h + b) * 64 + 16 * c);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         mma_f16(d, va[0], vb[0], va[1], vb[1], x.x, x.y);
         mma_f16(d, va[2], vb[2], va[3], vb[3], x.z, x.w);
-        weigh(acc.a[b], d, make_float2(sx0[b], sx1[b]), e8m0_weight(h ? w0.y : w0.x, b),
-              e8m0_weight(h ? w1.y : w1.x, b));
+        weigh(acc.a[b & 1], d, make_float2(__uint_as_float(sx0[b]), __uint_as_float(sx1[b])),
+              e8m0_weight(h ? w0.y : w0.x, b), e8m0_weight(h ? w1.y : w1.x, b));
       }
     }
   } else {
-    const uint8_t *a0 = o.tile + o0 + ((c << 4) ^ x0), *a1 = o.tile + o1 + ((c << 4) ^ x1);
+    const uint32_t a0 = o.a0 + ((c << 4) ^ x0), a1 = o.a1 + ((c << 4) ^ x1);
     float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // halves of the line, 64 bytes
-      const uint32_t flip = h ? 64u : 0u;
-      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(a0) ^ flip);
-      const uint4 b = *reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(a1) ^ flip);
+      const uint4 a = lds128(h ? a0 ^ 64u : a0), b = lds128(h ? a1 ^ 64u : a1);
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
       if constexpr (kW == MOE_WDTYPE_BF16) {
-        const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 128 + h * 64 + 16 * c);
+        const uint4 x = lds128(o.x + h * 64 + 16 * c);
         mma_b16(acc.a[2 * h], aw[0], bw[0], aw[1], bw[1], x.x, x.y);
         mma_b16(acc.a[2 * h + 1], aw[2], bw[2], aw[3], bw[3], x.z, x.w);
       } else if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-        const uint4* xp = reinterpret_cast<const uint4*>(o.x + kl * 256 + h * 128 + 32 * c);
-        const uint4 xa = xp[0], xb = xp[1];
+        const uint4 xa = lds128(o.x + h * 128 + 32 * c), xb = lds128(o.x + h * 128 + 32 * c + 16);
         const uint32_t xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -305,14 +322,13 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, in
       } else {
         // NVFP4: the codes times their 16-input scale, exact in f16 (5 significant
         // bits, 2^-10 to 2688); 128 inputs a half, with one activation scale.
-        const uint32_t sa = *reinterpret_cast<const uint16_t*>(o.scales + o.c0 + l * 16 + h * 8 + 2 * c);
-        const uint32_t sb = *reinterpret_cast<const uint16_t*>(o.scales + o.c1 + l * 16 + h * 8 + 2 * c);
+        const uint32_t sa = lds16(o.c0 + h * 8 + 2 * c), sb = lds16(o.c1 + h * 8 + 2 * c);
         const uint32_t wa[2] = {f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sa, 0, 0x11))};
         const uint32_t wb[2] = {f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x00)), f16x2_of_e4m3x2(__byte_perm(sb, 0, 0x11))};
         float e[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 x = *reinterpret_cast<const uint4*>(o.x + kl * 512 + h * 256 + 64 * j + 16 * c);
+          const uint4 x = lds128(o.x + h * 256 + 64 * j + 16 * c);
           uint32_t va[4], vb[4];
           f16_of_e2m1x8(aw[j], va);
           f16_of_e2m1x8(bw[j], vb);
@@ -324,22 +340,28 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, int l, in
           mma_f16(e[j & 1], va[0], vb[0], va[1], vb[1], x.x, x.y);
           mma_f16(e[j & 1], va[2], vb[2], va[3], vb[3], x.z, x.w);
         }
-        const float2 sx = make_float2(o.s0[2 * kl + h], o.s1[2 * kl + h]);
-        weigh(acc.a[0], e[0], sx, 1.0f, 1.0f);
-        weigh(acc.a[1], e[1], sx, 1.0f, 1.0f);
+        const float sx0 = __uint_as_float(lds32(o.s0 + 4 * h)), sx1 = __uint_as_float(lds32(o.s1 + 4 * h));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc.a[0][2 * i] = fmaf(e[0][2 * i] + e[1][2 * i], sx0, acc.a[0][2 * i]);
+          acc.a[0][2 * i + 1] = fmaf(e[0][2 * i + 1] + e[1][2 * i + 1], sx1, acc.a[0][2 * i + 1]);
+        }
       }
     }
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[0][i] += d[1][i];
-      weigh(acc.a[0], d[0], make_float2(o.s0[kl], o.s1[kl]), sb0, sb1);
+      const float sx0 = __uint_as_float(lds32(o.s0)), sx1 = __uint_as_float(lds32(o.s1));
+      acc.a[0][0] = fmaf(d[0][0] + d[1][0], sx0 * sb0, acc.a[0][0]);
+      acc.a[0][1] = fmaf(d[0][1] + d[1][1], sx1 * sb0, acc.a[0][1]);
+      acc.a[0][2] = fmaf(d[0][2] + d[1][2], sx0 * sb1, acc.a[0][2]);
+      acc.a[0][3] = fmaf(d[0][3] + d[1][3], sx1 * sb1, acc.a[0][3]);
     }
   }
 }
 
 // 8 values of a row (inputs 8 v .. 8 v + 7; all lanes of the warp take part, `live`
 // ones hold values) into the operand row at `row` with scales behind it. FP8:
-// kDivide quantises by IEEE quotients (x), else by the scale's reciprocal (h).
+// kDivide quantises by IEEE quotients (x, as moe_quantize_act defines it), else by
+// products with approximate reciprocals (h, whose own fp32 noise is larger).
 template <int kW, bool kDivide>
 __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v, const float (&f)[8], bool live) {
   using F = Fmt<kW>;
@@ -358,8 +380,8 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
       // (A NaN fails the comparison, keeps scale 1 and becomes a NaN code.)
       const float amax = __uint_as_float(m);
-      s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-      const float r = kDivide ? 1.0f : __frcp_rn(s);
+      s = amax > 0.0f ? (kDivide ? __fdiv_rn(amax, 448.0f) : amax * (1.0f / 448.0f)) : 1.0f;
+      const float r = kDivide ? 1.0f : __fdividef(1.0f, s);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 q = kDivide ? make_float2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s))
@@ -392,16 +414,18 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
 
 // ------------------------------------------------------------------ router --
 
-// One CTA per expert: logits [T, E] of all tokens, fp32 sums in a fixed order. The
-// CTAs after those bring x into the operand layout, rows of Smem::pitch(H) bytes.
-// CTA 0 also clears the status record and the second kernel's barrier counter.
+// Two experts per CTA: logits [T, E] of all tokens, fp32 sums in a fixed order, a
+// thread's loads all issued together. The CTAs after those bring x into the operand
+// layout, rows of Smem::pitch(H) bytes. CTA 0 also clears the status record and the
+// second kernel's barrier counter.
 template <int kW>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewParams p) {
   using L = Smem<kW>;
   pdl_wait();
   pdl_trigger();  // after the wait: the next kernel may read everything that this one may
-  if ((int)blockIdx.x >= p.E) {
-    const int per_row = p.H / 8, v = ((int)blockIdx.x - p.E) * kRouterThreads + threadIdx.x;  // 16 k per row
+  const int router_ctas = (p.E + kRouterExperts - 1) / kRouterExperts;
+  if ((int)blockIdx.x >= router_ctas) {
+    const int per_row = p.H / 8, v = ((int)blockIdx.x - router_ctas) * kRouterThreads + threadIdx.x;  // 16 k per row
     const bool live = v < p.T * per_row;
     const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(p.x) + v) : make_uint4(0, 0, 0, 0);
     const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw);
@@ -419,40 +443,68 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewPar
     for (int i = threadIdx.x; i < (int)(kStatusBytes / 4); i += kRouterThreads) p.status[i] = 0;
     if (threadIdx.x == 0) *p.counter = 0;
   }
-  __shared__ float part[kRouterThreads / 32][kFewMaxTokens];
-  const int e = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (int64_t)e * (p.H / 8);
-  float acc[kFewMaxTokens];
+  __shared__ float part[kRouterThreads / 32][kRouterExperts][kFewMaxTokens];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, nvec = p.H / 8;
+  const int e0 = blockIdx.x * kRouterExperts;
+  const uint4* w[kRouterExperts];
 #pragma unroll
-  for (int t = 0; t < kFewMaxTokens; ++t) acc[t] = 0.0f;
-  for (int v = threadIdx.x; v < p.H / 8; v += kRouterThreads) {
-    const uint4 wv = __ldg(w + v);
-    const __nv_bfloat162* wb = reinterpret_cast<const __nv_bfloat162*>(&wv);
+  for (int e = 0; e < kRouterExperts; ++e)
+    w[e] = reinterpret_cast<const uint4*>(p.router_w) + (int64_t)min(e0 + e, p.E - 1) * nvec;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x);
+  float acc[kRouterExperts][kFewMaxTokens];
 #pragma unroll
-    for (int t = 0; t < kFewMaxTokens; ++t) {
-      if (t >= p.T) break;
-      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)t * (p.H / 8) + v);
-      const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(&xv);
+  for (int e = 0; e < kRouterExperts; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = __bfloat1622float2(wb[i]), b = __bfloat1622float2(xb[i]);
-        acc[t] = fmaf(a.x, b.x, acc[t]);
-        acc[t] = fmaf(a.y, b.y, acc[t]);
+    for (int t = 0; t < kFewMaxTokens; ++t) acc[e][t] = 0.0f;
+  for (int v0 = threadIdx.x; v0 < nvec; v0 += 2 * kRouterThreads) {
+    uint4 wv[2][kRouterExperts], xv[2][kFewMaxTokens];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int v = v0 + i * kRouterThreads;
+      if (v >= nvec) break;
+#pragma unroll
+      for (int e = 0; e < kRouterExperts; ++e) wv[i][e] = __ldcs(w[e] + v);
+#pragma unroll
+      for (int t = 0; t < kFewMaxTokens; ++t)
+        if (t < p.T) xv[i][t] = __ldg(x + t * nvec + v);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (v0 + i * kRouterThreads >= nvec) break;
+#pragma unroll
+      for (int t = 0; t < kFewMaxTokens; ++t) {
+        if (t >= p.T) break;
+        const __nv_bfloat162* xb = reinterpret_cast<const __nv_bfloat162*>(&xv[i][t]);
+#pragma unroll
+        for (int e = 0; e < kRouterExperts; ++e) {
+          const __nv_bfloat162* wb = reinterpret_cast<const __nv_bfloat162*>(&wv[i][e]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = __bfloat1622float2(wb[j]), b = __bfloat1622float2(xb[j]);
+            acc[e][t] = fmaf(a.x, b.x, acc[e][t]);
+            acc[e][t] = fmaf(a.y, b.y, acc[e][t]);
+          }
+        }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < kFewMaxTokens; ++t) {
+  for (int e = 0; e < kRouterExperts; ++e) {
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-    if (lane == 0) part[warp][t] = acc[t];
+    for (int t = 0; t < kFewMaxTokens; ++t) {
+      if (t >= p.T) break;
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) acc[e][t] += __shfl_xor_sync(0xffffffffu, acc[e][t], o);
+      if (lane == 0) part[warp][e][t] = acc[e][t];
+    }
   }
   __syncthreads();
-  if (threadIdx.x < p.T) {
+  const int e = threadIdx.x / kFewMaxTokens, t = threadIdx.x % kFewMaxTokens;
+  if (e < kRouterExperts && e0 + e < p.E && t < p.T) {
     float l = 0.0f;
-    for (int i = 0; i < kRouterThreads / 32; ++i) l += part[i][threadIdx.x];
-    if (p.bias) l += p.bias[e];
-    p.logits[threadIdx.x * p.E + e] = l;
+    for (int i = 0; i < kRouterThreads / 32; ++i) l += part[i][e][t];
+    if (p.bias) l += p.bias[e0 + e];
+    p.logits[t * p.E + e0 + e] = l;
   }
 }
 
@@ -495,11 +547,20 @@ struct GateUpWalk {
   }
 };
 
-// This CTA's even share of `experts` experts from list entry u0.
-__device__ __forceinline__ GateUpWalk gate_up_walk(const FewParams& p, int u0, int experts) {
-  const int per = p.I / 8, total = experts * per;
-  return GateUpWalk{(int)((int64_t)total * blockIdx.x / gridDim.x), (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x),
-                    u0, per};
+// This CTA's even share of the shared expert, and of the routed ones after it.
+__device__ __forceinline__ int share(const FewParams& p, int experts, int cta) {
+  return (int)((int64_t)experts * (p.I / 8) * cta / gridDim.x);
+}
+__device__ __forceinline__ GateUpWalk shared_walk(const FewParams& p) {
+  return GateUpWalk{share(p, p.S, blockIdx.x), share(p, p.S, blockIdx.x + 1), 0, p.I / 8};
+}
+__device__ __forceinline__ GateUpWalk routed_walk(const FewParams& p, int U) {
+  // The two shares together are even where a CTA has a tile of each expert or more
+  // (then no CTA's routed share comes out negative).
+  auto at = [&](int cta) {
+    return p.I / 8 >= (int)gridDim.x ? share(p, U, cta) - share(p, p.S, cta) : share(p, U - p.S, cta);
+  };
+  return GateUpWalk{at(blockIdx.x), at(blockIdx.x + 1), p.S, p.I / 8};
 }
 
 // Down: this CTA's output rows [r0, r0 + rows), in groups of p.group_rows (a multiple
@@ -546,29 +607,25 @@ struct Producer {
   uint32_t issued = 0, issued_phase = 0;  // per slot: loaded at all, and the phase of the last load
 };
 
-// Loads the K slabs of a tile: boxes of `rows` rows from row0 and slab_bytes of each
-// (with two maps, the same rows of both: gate and up). One thread, and as few instructions per
-// stage as possible: at the HBM rate a stage takes about 700 clocks, and a TMA
-// instruction costs its thread more than 100.
-template <int kW, bool kScales, bool kTwoMaps>
-__device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>& pr, const CUtensorMap* m0,
-                                          const CUtensorMap* m1, int row0, int rows, int slab_bytes, int slabs,
+// Loads the K slabs of a tile: a box of rows from row0 and slab_bytes of each to
+// `offset` in every slot. One thread and one TMA instruction per stage (it costs the
+// thread more than 100 clocks, and at the HBM rate a stage takes about 350): gate and
+// up rows, and the scale bytes of each, have threads of their own.
+template <int kW, bool kScales>
+__device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>& pr, const CUtensorMap* m, int row0,
+                                          int offset, int bytes, int slab_bytes, int slabs, bool both,
                                           volatile int* abort_flag) {
   using F = Fmt<kW>;
   constexpr int kSlot = kRows * (kScales ? F::kScaleSlab : F::kSlab);
-  const uint32_t bytes = (uint32_t)((kTwoMaps ? 2 : 1) * rows * slab_bytes);
   for (int k = 0; k < slabs; ++k) {
     const int st = pr.rg.stage;
     if (!mbar_wait(&pr.empty[st], pr.rg.phase ^ 1u, p.status, abort_flag, 0x2001, k, p.wait_ns)) return false;
     uint64_t* bar = &pr.full[st];
-    mbar_arrive_expect_tx(bar, bytes);
-    uint8_t* dst = pr.dst + st * kSlot;
-    auto load = [&](uint8_t* to, const CUtensorMap* m) {
-      if constexpr (kScales) tma_load_2d(to, m, bar, k * slab_bytes, row0);
-      else tma_load_rows(to, m, bar, row0, k * (slab_bytes / 128));
-    };
-    load(dst, m0);
-    if (kTwoMaps) load(dst + rows * slab_bytes, m1);
+    mbar_arrive_expect_tx(bar, (uint32_t)bytes);
+    if (both) mbar_arrive(bar);  // nothing comes from the other thread
+    uint8_t* dst = pr.dst + st * kSlot + offset;
+    if constexpr (kScales) tma_load_2d(dst, m, bar, k * slab_bytes, row0);
+    else tma_load_rows(dst, m, bar, row0, k * (slab_bytes / 128));
     pr.issued |= 1u << st;
     pr.issued_phase ^= ((pr.issued_phase >> st ^ pr.rg.phase) & 1u) << st;
     pr.rg.step(pr.n_stages);
@@ -576,62 +633,70 @@ __device__ __forceinline__ bool load_tile(const FewParams& p, Producer<kScales>&
   return true;
 }
 
-// Everything a producer warp does (lane 0 loads).
-template <int kW, bool kScales>
+// Everything a producing thread does: kUp false: the gate rows and, after them, the
+// down rows; true: the up rows only.
+template <int kW, bool kScales, bool kUp>
 __device__ __forceinline__ void produce(const FewParams& p, const FewMaps& tm, uint8_t* dst, uint64_t* full,
                                         uint64_t* empty, const int* list, volatile int* n_list, volatile int* abort_flag,
                                         int h_slabs, const DownRows& dr, int lane) {
+  constexpr int kBytes = kScales ? Fmt<kW>::kScaleSlab : Fmt<kW>::kSlab;
   Producer<kScales> pr{dst, full, empty, p.n_stages};
   bool ok = p.inject != 1;
-  const CUtensorMap *g = kScales ? &tm.s1 : &tm.w1, *u = kScales ? &tm.s3 : &tm.w3, *d = kScales ? &tm.s2 : &tm.w2;
-  const CUtensorMap *sg = kScales ? &tm.ss1 : &tm.sw1, *su = kScales ? &tm.ss3 : &tm.sw3,
-                    *sd = kScales ? &tm.ss2 : &tm.sw2;
-  auto gate_up = [&](GateUpWalk w) {
+  const CUtensorMap* w = kScales ? (kUp ? &tm.s3 : &tm.s1) : (kUp ? &tm.w3 : &tm.w1);
+  const CUtensorMap* sw = kScales ? (kUp ? &tm.ss3 : &tm.ss1) : (kUp ? &tm.sw3 : &tm.sw1);
+  auto gate_up = [&](GateUpWalk walk) {
     Tile t;
-    while (ok && w.next(t)) {
+    while (ok && walk.next(t)) {
       const bool sh = p.S && t.u == 0;
-      ok = load_tile<kW, kScales, true>(p, pr, sh ? sg : g, sh ? su : u, (sh ? 0 : list[t.u]) * p.I + t.r0, 8,
-                                        kScales ? Fmt<kW>::kScaleSlab : Fmt<kW>::kSlab, h_slabs, abort_flag);
+      ok = load_tile<kW, kScales>(p, pr, sh ? sw : w, (sh ? 0 : list[t.u]) * p.I + t.r0, kUp ? 8 * kBytes : 0, 8 * kBytes,
+                                  kBytes, h_slabs, false, abort_flag);
     }
   };
-  if (lane == 0) gate_up(gate_up_walk(p, 0, p.S));  // the shared expert: needs no routing
+  if (lane == 0) gate_up(shared_walk(p));  // the shared expert: needs no routing
   __syncwarp();
-  named_bar_sync(1, kThreads);  // the expert list is ready
-  if (lane != 0) return;
-  const int U = *n_list;
-  gate_up(gate_up_walk(p, p.S, U - p.S));
-  const int slab_bytes = dr.lines * (kScales ? Fmt<kW>::kScaleSlab / (Fmt<kW>::kSlab / kLine) : kLine);
-  for (int i = 0; i < U && ok; ++i) {
-    const int e = down_entry(i, U, p.S);
-    const bool sh = p.S && e == 0;
-    const int base = (sh ? 0 : list[e]) * p.H;
-    for (int q = 0; q < dr.groups && ok; ++q)
-      ok = load_tile<kW, kScales, false>(p, pr, sh ? sd : d, nullptr, base + dr.first(q), dr.per, slab_bytes, dr.slabs,
-                                         abort_flag);
+  named_bar_sync(1, Smem<kW>::kThreads);  // the expert list is ready
+  if (lane == 0) {
+    const int U = *n_list;
+    gate_up(routed_walk(p, U));
+    if (!kUp) {
+      const CUtensorMap *d = kScales ? &tm.s2 : &tm.w2, *sd = kScales ? &tm.ss2 : &tm.sw2;
+      const int slab_bytes = dr.lines * (kScales ? Fmt<kW>::kScaleSlab / (Fmt<kW>::kSlab / kLine) : kLine);
+      for (int i = 0; i < U && ok; ++i) {
+        const int e = down_entry(i, U, p.S);
+        const bool sh = p.S && e == 0;
+        const int base = (sh ? 0 : list[e]) * p.H;
+        for (int q = 0; q < dr.groups && ok; ++q)
+          ok = load_tile<kW, kScales>(p, pr, sh ? sd : d, base + dr.first(q), 0, dr.per * slab_bytes, slab_bytes, dr.slabs,
+                                      true, abort_flag);
+      }
+    }
+    // Let every copy land before the thread leaves (the others wait for them too, unless a
+    // wait gave up; the slots of the up rows are used again by then).
+    for (int s = 0; s < p.n_stages && (!kUp || !ok); ++s) {
+      if (!(pr.issued & (1u << s))) continue;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&full[s], (pr.issued_phase >> s) & 1u) && global_timer_ns() - t0 < 200000000ull) {}
+    }
   }
-  // Let every copy land before the thread leaves (the others wait for them too, unless a wait gave up).
-  for (int s = 0; s < p.n_stages; ++s) {
-    if (!(pr.issued & (1u << s))) continue;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&full[s], (pr.issued_phase >> s) & 1u) && global_timer_ns() - t0 < 200000000ull) {}
-  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- the layer --
 
 template <int kW>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
     few_experts_kernel(const FewParams p, const __grid_constant__ FewMaps tm) {
   using F = Fmt<kW>;
   using L = Smem<kW>;
+  constexpr int kWarps = L::kWarps, kTeams = L::kTeams, kConsumers = L::kConsumers, kThreads = L::kThreads;
   constexpr bool kScaleBytes = F::kScaleSlab != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + kMaxRing;
-  uint64_t* pfull = empty + kMaxRing;    // a warp's partial sums are in its buffer
-  uint64_t* pempty = pfull + kWarps;     // ... and have been read
-  uint64_t* hfull = pempty + kWarps;     // an expert's rows of h are in shared memory
+  uint64_t* pfull = empty + kMaxRing;    // a team's partial sums are in its buffers
+  uint64_t* pempty = pfull + kTeams;     // ... and have been read
+  uint64_t* hfull = pempty + kTeams;     // an expert's rows of h are in shared memory
   uint64_t* hempty = hfull + kHRing;     // ... and have been used by all of its stages
   uint64_t* h_ready = hempty + kHRing;   // every CTA's h is written
   uint64_t* x_ready = h_ready + 1;       // x is in shared memory
@@ -663,16 +728,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < n_stages; ++i) {
-      mbar_init(&full[i], kScaleBytes ? 2 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&full[i], kScaleBytes ? 4 : 2);
+      mbar_init(&empty[i], kTeam);
     }
-    for (int i = 0; i < kWarps; ++i) {
-      mbar_init(&pfull[i], 1);
+    for (int i = 0; i < kTeams; ++i) {
+      mbar_init(&pfull[i], kTeam);
       mbar_init(&pempty[i], 1);
     }
     for (int i = 0; i < kHRing; ++i) {
       mbar_init(&hfull[i], kPrep);
-      mbar_init(&hempty[i], dr.rows ? dr.groups * dr.slabs : 1);
+      mbar_init(&hempty[i], dr.rows ? dr.groups * dr.slabs * kTeam : 1);
     }
     mbar_init(h_ready, 1);
     mbar_init(x_ready, 1);
@@ -687,115 +752,124 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   if (warp == kWarps + kAcc + kPrep) {
-    produce<kW, false>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
+    produce<kW, false, false>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
     return;
   }
-  if (warp == kWarps + kAcc + kPrep + 1) {
-    if constexpr (kScaleBytes)
-      produce<kW, true>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
-    else
-      named_bar_arrive(1, kThreads);
+  if (kScaleBytes && warp == kWarps + kAcc + kPrep + 1) {
+    produce<kW, true, false>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
     return;
   }
 
+  // The first of the warps that bring h load the up rows and their scale bytes before.
+  constexpr int kUpWarps = kScaleBytes ? 2 : 1;
+  constexpr int kPrep0 = kWarps + kAcc;
+  if (warp == kPrep0) {
+    produce<kW, false, true>(p, tm, tiles, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
+  } else if (kScaleBytes && warp == kPrep0 + 1) {
+    produce<kW, true, true>(p, tm, scales, full, empty, list, n_list, abort_flag, h_slabs, dr, lane);
+  }
   const int g = lane / 4, c = lane % 4;
-  pdl_wait();  // the logits, x in the operand layout, the cleared counter
-  if (threadIdx.x == kConsumers - 32) {  // (a warp without a token to select for)
-    mbar_arrive_expect_tx(x_ready, (uint32_t)(T * xpitch));
-    bulk_load(act, p.xrows, (uint32_t)(T * xpitch), x_ready);
-  }
-  if (warp < T) {
-    // Top-k of token `warp`: order-preserving integer keys, ties to the lower
-    // index, a NaN below everything; a taken expert's key is 0.
-    constexpr int kPer = kMaxExperts / 32;
-    uint32_t key[kPer];
+  constexpr int kOthers = kConsumers - kUpWarps * 32;  // threads of the selection
+  if (warp < kPrep0 || warp >= kPrep0 + kUpWarps) {
+    pdl_wait();  // the logits, x in the operand layout, the cleared counter
+    if (threadIdx.x == kConsumers - 32) {  // (a warp without a token to select for)
+      mbar_arrive_expect_tx(x_ready, (uint32_t)(T * xpitch));
+      bulk_load(act, p.xrows, (uint32_t)(T * xpitch), x_ready);
+    }
+    if (warp < T) {
+      // Top-k of token `warp`: order-preserving integer keys, ties to the lower
+      // index, a NaN below everything; a taken expert's key is 0.
+      constexpr int kPer = kMaxExperts / 32;
+      uint32_t key[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = i * 32 + lane;
-      key[i] = 0;
-      if (e < p.E) {
-        const uint32_t b = __float_as_uint(__ldcg(p.logits + warp * p.E + e));
-        key[i] = (b & 0x7fffffffu) > 0x7f800000u ? 1u : ((b >> 31) ? ~b : (b | 0x80000000u));
-        if (key[i] == 0x7fffffffu) key[i] = 0x80000000u;  // -0 equals +0
+      for (int i = 0; i < kPer; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = 0;
+        if (e < p.E) {
+          const uint32_t b = __float_as_uint(__ldcg(p.logits + warp * p.E + e));
+          key[i] = (b & 0x7fffffffu) > 0x7f800000u ? 1u : ((b >> 31) ? ~b : (b | 0x80000000u));
+          if (key[i] == 0x7fffffffu) key[i] = 0x80000000u;  // -0 equals +0
+        }
+      }
+      float w = 0.0f, l0 = 0.0f;
+      int mine = 0;
+      for (int j = 0; j < p.k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        uint32_t at = 0xffffffffu;
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i)
+          if (key[i] == best) at = i * 32 + lane;
+        at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (at == (uint32_t)(i * 32 + lane)) key[i] = 0;
+        const float l = best == 1u ? __uint_as_float(0x7fffffffu)
+                                   : __uint_as_float((best >> 31) ? best ^ 0x80000000u : ~best);
+        if (j == 0) l0 = l;
+        if (lane == j) {
+          w = l;
+          mine = (int)at;
+        }
+      }
+      // Gates: the chosen logits' softmax.
+      const float ex = lane < p.k ? expf(w - l0) : 0.0f;
+      float z = ex;
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (lane < p.k) {
+        const float gate = ex / z;
+        top_idx[warp * p.k + lane] = mine;
+        top_w[warp * p.k + lane] = gate;
+        atomicOr(&bits[mine >> 5], 1u << (mine & 31));
+        if (blockIdx.x == 0 && p.topk_idx) {
+          p.topk_idx[warp * p.k + lane] = mine;
+          p.topk_w[warp * p.k + lane] = gate;
+        }
       }
     }
-    float w = 0.0f, l0 = 0.0f;
-    int mine = 0;
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t best = 0;
+    named_bar_sync(2, kOthers);
+    if (warp == 0) {
+      // The distinct experts, ascending, after the shared one.
+      const uint32_t word = lane < 16 ? bits[lane] : 0u;
+      int sum = __popc(word);
+      const int own = sum;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      uint32_t at = 0xffffffffu;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i)
-        if (key[i] == best) at = i * 32 + lane;
-      at = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (at == (uint32_t)(i * 32 + lane)) key[i] = 0;
-      const float l = best == 1u ? __uint_as_float(0x7fffffffu)
-                                 : __uint_as_float((best >> 31) ? best ^ 0x80000000u : ~best);
-      if (j == 0) l0 = l;
-      if (lane == j) {
-        w = l;
-        mine = (int)at;
+      for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
       }
-    }
-    // Gates: the chosen logits' softmax.
-    const float ex = lane < p.k ? expf(w - l0) : 0.0f;
-    float z = ex;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (lane < p.k) {
-      const float gate = ex / z;
-      top_idx[warp * p.k + lane] = mine;
-      top_w[warp * p.k + lane] = gate;
-      atomicOr(&bits[mine >> 5], 1u << (mine & 31));
-      if (blockIdx.x == 0 && p.topk_idx) {
-        p.topk_idx[warp * p.k + lane] = mine;
-        p.topk_w[warp * p.k + lane] = gate;
+      int at = S + sum - own;
+      if (lane < 16) prefix[lane] = at;
+      for (uint32_t b = word; b; b &= b - 1) list[at++] = lane * 32 + __ffs(b) - 1;
+      if (lane == 31) *n_list = S + sum;
+      if (S && lane == 0) {
+        list[0] = p.E;
+        used[0] = (1u << T) - 1u;
       }
+      if (S && lane < T) gates[lane] = 1.0f;
     }
-  }
-  named_bar_sync(2, kConsumers);
-  if (warp == 0) {
-    // The distinct experts, ascending, after the shared one.
-    const uint32_t word = lane < 16 ? bits[lane] : 0u;
-    int sum = __popc(word);
-    const int own = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+    named_bar_sync(2, kOthers);
+    for (int i = threadIdx.x; i < T * p.k; i += kConsumers) {
+      const int e = top_idx[i], t = i / p.k;
+      const int u = prefix[e >> 5] + __popc(bits[e >> 5] & ((1u << (e & 31)) - 1u));
+      gates[u * kFewMaxTokens + t] = top_w[i];
+      atomicOr(&used[u], 1u << t);
     }
-    int at = S + sum - own;
-    if (lane < 16) prefix[lane] = at;
-    for (uint32_t b = word; b; b &= b - 1) list[at++] = lane * 32 + __ffs(b) - 1;
-    if (lane == 31) *n_list = S + sum;
-    if (S && lane == 0) {
-      list[0] = p.E;
-      used[0] = (1u << T) - 1u;
-    }
-    if (S && lane < T) gates[lane] = 1.0f;
+    // The expert list is ready. The producing threads wait for it; the others do not
+    // wait for them, whose ring may be full of the shared expert's rows. (The warps that
+    // bring h load the up rows and their scale bytes until then.)
+    named_bar_sync(2, kOthers);
+    named_bar_arrive(1, kThreads);
   }
-  named_bar_sync(2, kConsumers);
-  for (int i = threadIdx.x; i < T * p.k; i += kConsumers) {
-    const int e = top_idx[i], t = i / p.k;
-    const int u = prefix[e >> 5] + __popc(bits[e >> 5] & ((1u << (e & 31)) - 1u));
-    gates[u * kFewMaxTokens + t] = top_w[i];
-    atomicOr(&used[u], 1u << t);
-  }
-  // The expert list is ready. The producers wait for it here; the consumers do not
-  // wait for the producers, whose ring may be full of the shared expert's rows.
-  named_bar_arrive(1, kThreads);
-  named_bar_sync(2, kConsumers);
   const int U = *n_list;
 
   // Stages are numbered in the producers' order; stage n is in ring slot n % n_stages
-  // and belongs to warp n % A, whose partial sums go to buffer n % A.
-  const int A = min(kWarps, n_stages);
-  const GateUpWalk walk0 = gate_up_walk(p, 0, S), walk1 = gate_up_walk(p, S, U - S);
+  // and belongs to team n % A of kTeam warps, each of which takes every kTeam-th line.
+  const int A = min(kTeams, n_stages);
+  const GateUpWalk walk0 = shared_walk(p), walk1 = routed_walk(p, U);
   const int tiles0 = walk0.end - walk0.pos;
   const int gu_tiles = tiles0 + walk1.end - walk1.pos, gu_stages = gu_tiles * h_slabs;
   const int per_entry = dr.groups * dr.slabs;  // stages of a list entry in the down phase
@@ -804,8 +878,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp < kWarps) {
+    const int team = warp / kTeam, tw = warp % kTeam;
     // ------------------------------------------------------------ multiply --
-    Ring rg, pr;  // this warp's next ring slot; phase of its buffer
+    Ring rg, pr;  // this team's next ring slot; phase of its buffers
     auto advance = [&](int n) {
       rg.stage += n;
       while (rg.stage >= n_stages) {
@@ -813,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rg.phase ^= 1u;
       }
     };
-    advance(warp);
+    advance(team);
     // FP8: a stage's weight scales: lane l < 8 holds that of rows 0..7 (down: of the
     // tile's first row's block) and K block l, lane 8 + l that of rows 8..15 (of its
     // last row's block); fetched a turn ahead.
@@ -842,9 +917,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __ldg(f + kb);
     };
     if (ok) ok = warp_wait<false>(x_ready, 0, p.status, abort_flag, 0x200d, 0, p.wait_ns);
-    float next_scale = warp < A ? fetch_scale(warp) : 0.0f;
+    const uint32_t act_a = smem_u32(act), tiles_a = smem_u32(tiles), scales_a = smem_u32(scales);
+    float next_scale = team < A ? fetch_scale(team) : 0.0f;
     bool x_used = true;
-    for (int n = warp; n < all_stages && warp < A; n += A) {
+    for (int n = team; n < all_stages && team < A; n += A) {
       const float scale = next_scale;
       next_scale = fetch_scale(n + A);
       const bool gate_up = n < gu_stages;
@@ -855,20 +931,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The stage's lines, the token rows, and where the weight rows lie: line after line
       // of eight gate rows, and the same of the up rows behind them; or of a group's rows.
-      int kl0, lines, entry = 0, group = 0;
-      Operands o;
+      int kl0, lines, entry = 0, group = 0, per = 8;
+      uint32_t xa, s0a, s1a;
       if (gate_up) {
         kl0 = by_h.rem(n) * (F::kSlab / kLine);
         lines = min(F::kSlab / kLine, h_bytes / kLine - kl0);
-        o.x = act + min(g, T - 1) * xpitch;  // lanes past the last token repeat it; their columns are not used
-        o.s0 = reinterpret_cast<const float*>(act + min(2 * c, T - 1) * xpitch + L::scales_at(H));
-        o.s1 = reinterpret_cast<const float*>(act + min(2 * c + 1, T - 1) * xpitch + L::scales_at(H));
+        // Lanes past the last token repeat it; their columns are not used.
+        xa = act_a + min(g, T - 1) * xpitch;
+        s0a = act_a + min(2 * c, T - 1) * xpitch + L::scales_at(H);
+        s1a = act_a + min(2 * c + 1, T - 1) * xpitch + L::scales_at(H);
       } else {
         entry = by_entry.quot(n - gu_stages);
         const int m = n - gu_stages - entry * per_entry, u = down_entry(entry, U, S);
         group = by_i.quot(m);
         kl0 = (m - group * dr.slabs) * dr.lines;
         lines = min(dr.lines, i_bytes / kLine - kl0);
+        per = dr.per;
         if (ok)
           ok = warp_wait<false>(&hfull[entry % kHRing], (uint32_t)(entry / kHRing) & 1u, p.status, abort_flag, 0x2005, n,
                                 p.wait_ns);
@@ -878,62 +956,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = ok ? by_rows.rem(first[entry]) : 0;
         auto row_of = [&](int tok) {
           const int r = row0 + ((mask >> tok) & 1u ? __popc(mask & ((1u << tok) - 1u)) : 0);
-          return act + (r >= h_rows ? r - h_rows : r) * hpitch;
+          return act_a + (r >= h_rows ? r - h_rows : r) * hpitch;
         };
-        o.x = row_of(g);
-        o.s0 = reinterpret_cast<const float*>(row_of(2 * c) + L::scales_at(I));
-        o.s1 = reinterpret_cast<const float*>(row_of(2 * c + 1) + L::scales_at(I));
+        xa = row_of(g);
+        s0a = row_of(2 * c) + L::scales_at(I);
+        s1a = row_of(2 * c + 1) + L::scales_at(I);
       }
-      // Stage n's slot held stage n - n_stages before, which another warp may not even
+      // Per line: bytes of activations, and of their scales.
+      constexpr uint32_t kXLine = 128 * F::kPer2, kSLine = F::kBlock ? 64 * F::kPer2 / F::kBlock * 4 : 0;
+      constexpr uint32_t kCLine = F::kScaleSlab / (F::kSlab / kLine);
+      xa += (kl0 + tw) * kXLine;
+      s0a += (kl0 + tw) * kSLine;
+      s1a += (kl0 + tw) * kSLine;
+      // Stage n's slot held stage n - n_stages before, which another team may not even
       // have seen land: its release is waited for first, or the parity of `full` could
       // be taken for the phase before. (The release before that one is certain: stage
       // n - A was loaded, so every stage up to n - A - n_stages has been released, and
       // A <= n_stages.)
       if (ok) ok = warp_wait<false>(&empty[rg.stage], rg.phase ^ 1u, p.status, abort_flag, 0x2007, n, p.wait_ns);
       if (ok) ok = warp_wait<false>(&full[rg.stage], rg.phase, p.status, abort_flag, 0x2002, n, p.wait_ns);
-      o.tile = tiles + rg.stage * (kRows * F::kSlab);
-      o.scales = scales + rg.stage * L::kStageScales;
       // Gate/up: one tile of 8 + 8 rows; down: one or two of 16 rows of the group.
+      const uint32_t tile = tiles_a + rg.stage * (kRows * F::kSlab), sc = scales_a + rg.stage * L::kStageScales;
       const int parts = gate_up ? 1 : (dr.count(group) + 15) / 16;
-      float4 sums[2];
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        if (part >= parts) break;
-        int sel0 = 0, sel1 = 8;
+      if (ok) ok = warp_wait<false>(&pempty[team], pr.phase ^ 1u, p.status, abort_flag, 0x2004, n, p.wait_ns);
+      // (Loops kept rolled: unrolled, the instruction fetch cost more than it hid.)
+#pragma unroll 1
+      for (int part = 0; part < parts; ++part) {
+        int sel0 = tw, sel1 = 8 + tw;
+        Operands o{0, 0, 0, 0, xa, s0a, s1a};
         if (gate_up) {
-          o.r0 = g * 128;
-          o.r1 = o.r0 + 8 * F::kSlab;
-          o.step = 8 * 128;
-          o.c0 = g * F::kScaleSlab;
-          o.c1 = (g + 8) * F::kScaleSlab;
+          o.a0 = tile + g * 128 + tw * (8 * 128);
+          o.a1 = o.a0 + 8 * F::kSlab;
+          o.c0 = sc + g * F::kScaleSlab + tw * kCLine;
+          o.c1 = o.c0 + 8 * F::kScaleSlab;
         } else {
           // (Rows past the group repeat its last one; their sums are not used.)
-          const int a = min(16 * part + g, dr.per - 1), b = min(16 * part + g + 8, dr.per - 1);
-          o.r0 = a * 128;
-          o.r1 = b * 128;
-          o.step = dr.per * 128;
-          o.c0 = a * (dr.lines * F::kScaleSlab / (F::kSlab / kLine));
-          o.c1 = b * (dr.lines * F::kScaleSlab / (F::kSlab / kLine));
+          const int ra = min(16 * part + g, per - 1), rb = min(16 * part + g + 8, per - 1);
+          o.a0 = tile + (ra + tw * per) * 128;
+          o.a1 = tile + (rb + tw * per) * 128;
+          o.c0 = sc + (ra * dr.lines + tw) * kCLine;
+          o.c1 = sc + (rb * dr.lines + tw) * kCLine;
           if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
             const int top = dr.first(group) / 128;
-            sel0 = (dr.first(group) + a) / 128 != top ? 8 : 0;
-            sel1 = (dr.first(group) + b) / 128 != top ? 8 : 0;
+            sel0 = tw + ((dr.first(group) + ra) / 128 != top ? 8 : 0);
+            sel1 = tw + ((dr.first(group) + rb) / 128 != top ? 8 : 0);
           }
         }
+        const uint32_t step = per * 128 * kTeam;
         Sums acc;
         acc.clear();
         if (ok) {
-#pragma unroll(kW == MOE_WDTYPE_BF16 || kW == MOE_WDTYPE_FP8_E4M3 ? 2 : 1)
-          for (int l = 0; l < lines; ++l) {
+#pragma unroll 1
+          for (int l = tw; l < lines; l += kTeam) {
             float sb0 = 1.0f, sb1 = 1.0f;
             if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
-              sb0 = __shfl_sync(0xffffffffu, scale, sel0 + l);
-              sb1 = __shfl_sync(0xffffffffu, scale, sel1 + l);
+              sb0 = __shfl_sync(0xffffffffu, scale, sel0);
+              sb1 = __shfl_sync(0xffffffffu, scale, sel1);
+              sel0 += kTeam;
+              sel1 += kTeam;
             }
-            line_mma<kW>(acc, o, l, kl0 + l, sb0, sb1, lane);
+            line_mma<kW>(acc, o, sb0, sb1, lane);
+            o.a0 += step;
+            o.a1 += step;
+            o.c0 += kCLine * kTeam;
+            o.c1 += kCLine * kTeam;
+            o.x += kXLine * kTeam;
+            o.s0 += kSLine * kTeam;
+            o.s1 += kSLine * kTeam;
           }
         }
-        sums[part] = acc.total();
+        *reinterpret_cast<float4*>(red + warp * 256 + part * 128 + lane * 4) = acc.total();
       }
       __syncwarp();
       if (lane == 0) {
@@ -941,11 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!gate_up) mbar_arrive(&hempty[entry % kHRing]);
       }
       advance(A);
-      if (ok) ok = warp_wait<false>(&pempty[warp], pr.phase ^ 1u, p.status, abort_flag, 0x2004, n, p.wait_ns);
-      *reinterpret_cast<float4*>(red + warp * 256 + lane * 4) = sums[0];
-      if (parts > 1) *reinterpret_cast<float4*>(red + warp * 256 + 128 + lane * 4) = sums[1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[warp]);
+      if (lane == 0) mbar_arrive(&pfull[team]);
       pr.phase ^= 1u;
     }
     if (x_used) {
@@ -971,50 +1059,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_bar_sync(4, kPrep * 32);
     if (ok) ok = warp_wait<false>(x_done, 0, p.status, abort_flag, 0x200a, 0, p.wait_ns);
     if (ok) ok = warp_wait<false>(h_ready, 0, p.status, abort_flag, 0x200b, 0, p.wait_ns);
-    // The four warps share each row, 128 groups of 8 values a pass and two passes a
-    // step; a step's values are fetched while the step before is stored.
+    // The warps take the rows in turn; a row goes in steps of 96 groups of 8 values,
+    // and a step's values are fetched while the step before is stored.
+    constexpr int kBatch = 3;
+    const int groups = I / 8;
     struct Step {
-      int i, u, r, j;  // entry, its list index, row of the entry, first pass
+      int i, u, r, j;  // entry, its list index, row of the entry, first group
       uint32_t mask;   // the entry's tokens from this row on
     };
-    const int groups = I / 8, mine = me * 32 + lane;
-    auto start = [&](int i) {
-      Step st{i, 0, 0, 0, 0u};
-      if (i < U) {
-        st.u = down_entry(i, U, S);
+    auto settle = [&](Step st) {  // from row st.r on to this warp's next row, in whatever entry
+      while (true) {
+        for (; st.mask; ++st.r, st.mask &= st.mask - 1)
+          if ((first[st.i] + st.r) % kPrep == me) return st;
+        if (++st.i >= U) return st;
+        st.u = down_entry(st.i, U, S);
         st.mask = used[st.u];
+        st.r = 0;
       }
-      return st;
     };
     auto after = [&](Step st) {
-      st.j += 2;
-      if (st.j * 128 < groups) return st;
+      if (st.i >= U) return st;
+      st.j += 32 * kBatch;
+      if (st.j < groups) return st;
       st.j = 0;
       ++st.r;
       st.mask &= st.mask - 1;
-      return st.mask ? st : start(st.i + 1);
+      return settle(st);
     };
-    auto fetch = [&](const Step& st, float4 (&v)[4]) {
-      if (st.i >= U) return;
-      const float4* src = reinterpret_cast<const float4*>(p.h + ((int64_t)st.u * kFewMaxTokens + __ffs(st.mask) - 1) * I);
+    struct Values {
+      float4 v[2 * kBatch];
+    };
+    auto fetch = [&](const Step& st) {
+      Values o;
+      const float4* src = nullptr;
+      if (st.i < U)
+        src = reinterpret_cast<const float4*>(p.h + ((int64_t)st.u * kFewMaxTokens + __ffs(st.mask) - 1) * I) +
+              2 * (st.j + lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int g8 = (st.j + j) * 128 + mine;
-        v[2 * j] = g8 < groups ? __ldcg(src + 2 * g8) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[2 * j + 1] = g8 < groups ? __ldcg(src + 2 * g8 + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < kBatch; ++k) {
+        const bool live = src && st.j + 32 * k + lane < groups;
+        o.v[2 * k] = live ? __ldcg(src + 64 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        o.v[2 * k + 1] = live ? __ldcg(src + 64 * k + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      return o;
     };
-    int freed = 0;  // entries whose rows are free again
-    Step st = start(0);
-    float4 v[4];
-    fetch(st, v);
-    while (st.i < U) {
+    int freed = 0, told = 0;  // entries whose rows are free again, and that this warp has reported
+    Step st = settle(Step{0, down_entry(0, U, S), 0, 0, used[down_entry(0, U, S)]});
+    Values cur = fetch(st);
+#pragma unroll 1
+    while (true) {
+      // Every entry before this step's has this warp's rows.
+      __syncwarp();
+      for (; told < min(st.i, U); ++told)
+        if (lane == 0) mbar_arrive(&hfull[told % kHRing]);
+      if (st.i >= U) break;
       const Step nx = after(st);
-      float4 w[4];
-      fetch(nx, w);
-      if (st.r == 0 && st.j == 0) {
-        // Room for the entry's rows: first[] counts on from entry to entry, the oldest go first.
-        const int end = first[st.i] + __popc(st.mask);
+      const Values next = fetch(nx);
+      if (st.j == 0) {
+        // Room for the row: first[] counts on from entry to entry, the oldest go first.
+        const int end = first[st.i] + st.r + 1;
         while (ok && (freed <= st.i - kHRing || first[freed] < end - h_rows)) {
           ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c,
                                 st.i, p.wait_ns);
@@ -1023,20 +1126,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint8_t* row = act + by_rows.rem(first[st.i] + st.r) * hpitch;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int g8 = (st.j + j) * 128 + mine;
-        if (g8 - lane >= groups) break;
-        const float f[8] = {v[2 * j].x,     v[2 * j].y,     v[2 * j].z,     v[2 * j].w,
-                            v[2 * j + 1].x, v[2 * j + 1].y, v[2 * j + 1].z, v[2 * j + 1].w};
+      for (int k = 0; k < kBatch; ++k) {
+        const int g8 = st.j + 32 * k + lane;
+        const float f[8] = {cur.v[2 * k].x,     cur.v[2 * k].y,     cur.v[2 * k].z,     cur.v[2 * k].w,
+                            cur.v[2 * k + 1].x, cur.v[2 * k + 1].y, cur.v[2 * k + 1].z, cur.v[2 * k + 1].w};
         store_operand<kW, false>(row, L::scales_at(I), g8, f, g8 < groups);
       }
-      if (nx.i != st.i) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&hfull[st.i % kHRing]);
-      }
       st = nx;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = w[j];
+      cur = next;
     }
     return;
   }
@@ -1055,11 +1152,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i >= parts) break;
-      const float4 v = *reinterpret_cast<const float4*>(red + w * 256 + i * 128 + lane * 4);
-      s[i][0] += v.x;
-      s[i][1] += v.y;
-      s[i][2] += v.z;
-      s[i][3] += v.w;
+#pragma unroll
+      for (int k = 0; k < kTeam; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(red + (w * kTeam + k) * 256 + i * 128 + lane * 4);
+        s[i][0] += v.x;
+        s[i][1] += v.y;
+        s[i][2] += v.z;
+        s[i][3] += v.w;
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&pempty[w]);
@@ -1183,13 +1283,18 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
   const int smem = Smem<kW>::tile_offset(p.T, p.H, p.I, p.n_stages) + p.n_stages * kRows * Fmt<kW>::kSlab + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const unsigned x_ctas = (unsigned)ceil_div((int64_t)p.T * p.H / 8, kRouterThreads);
-  e = launch_pdl(few_router_kernel<kW>, dim3((unsigned)p.E + x_ctas), dim3(kRouterThreads), 0, s, 1, p);
+  // The router CTAs ask for the shared-memory split of the second kernel, whose CTAs
+  // could otherwise not start on their SMs before they end.
+  auto router = few_router_kernel<kW>;
+  e = cudaFuncSetAttribute(router, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = (unsigned)(ceil_div(p.E, kRouterExperts) + ceil_div((int64_t)p.T * p.H / 8, kRouterThreads));
+  e = launch_pdl(router, dim3(ctas), dim3(kRouterThreads), 0, s, 1, p);
   if (e != cudaSuccess) return e;
   // Cooperative: the CTAs wait for one another, so all of them have to be resident.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Smem<kW>::kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -42,15 +42,14 @@ inline FewRows few_rows(int wdtype, int H, int sms) {
   r.cta = (int)ceil_div(H / 4, sms) * 4;
   const int groups = (int)ceil_div(r.cta, 32);
   r.group = (int)ceil_div(r.cta / 4, groups) * 4;
-  const bool four = wdtype == MOE_WDTYPE_NVFP4 || wdtype == MOE_WDTYPE_MXFP4;
-  r.lines = (four ? 8192 : 16384) / (r.group * 128);
-  if (r.lines > (four ? 4 : 8)) r.lines = four ? 4 : 8;
+  r.lines = 16384 / (r.group * 128);
+  if (r.lines > 8) r.lines = 8;
   if (wdtype == MOE_WDTYPE_MXFP4) r.lines &= ~1;
   return r;
 }
 
 // Weight tensor maps: rows as [128 bytes, rows, lines], 128B-swizzled boxes of 8 rows
-// x 8 (BF16, FP8) or 4 lines (w1, w3), or as FewRows says (w2); 4-bit storage: scale
+// x 8 lines (w1, w3), or as FewRows says (w2); 4-bit storage: scale
 // bytes [rows, K / block] in boxes of the same rows and inputs.
 struct FewMaps {
   CUtensorMap w1, w3, w2, sw1, sw3, sw2, s1, s3, s2, ss1, ss3, ss2;
