@@ -29,6 +29,8 @@ int g_gemm_variant = MOE_GEMM_AUTO;
 constexpr int64_t kPairMinRows = 128;
 constexpr int64_t kSwapMinRows = 1;
 constexpr int64_t kSwapMaxRows = 16;
+// MXFP4: both GEMMs on pairs when the routed groups average this many rows.
+constexpr int64_t kMxPairMinRows = 96;
 // FP8 down GEMM: staged TMA stores of y when its groups average this many rows
 // and its K (the intermediate size) is at most this deep.
 constexpr int64_t kStoreYMinRows = 128;
@@ -319,7 +321,11 @@ enum GemmKind { kSingle = 0, kPair = 1, kSwap = 2 };
 GemmKind gemm_kind(bool gate_up, int64_t routed_rows, int n_experts, int wdtype) {
   const bool fp8 = wdtype == MOE_WDTYPE_FP8_E4M3;
   const bool nvfp4 = wdtype == MOE_WDTYPE_NVFP4;
-  if (wdtype == MOE_WDTYPE_MXFP4) return kSingle;  // one kernel for every group size
+  if (wdtype == MOE_WDTYPE_MXFP4)
+    return g_gemm_variant == MOE_GEMM_PAIR ||
+                   (g_gemm_variant == MOE_GEMM_AUTO && routed_rows >= kMxPairMinRows * (int64_t)n_experts)
+               ? kPair
+               : kSingle;
   switch (g_gemm_variant) {
     case MOE_GEMM_SINGLE: return kSingle;
     case MOE_GEMM_PAIR: return nvfp4 ? kSingle : kPair;
@@ -341,8 +347,8 @@ bool amaps(AMaps* a, const void* base, bool fp8, uint64_t inner, uint64_t rows) 
 // Both MXFP4 GEMMs (mxfp4_gemm.cu) over R rows of codes A [R, K/2] with E8M0
 // scales a_scale [R, K/32]: gate/up (out = h codes [R, I/2] and out_scale [R,
 // I/32], or fp32 sums if raw) or down (out = y [R, H] bf16).
-int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, int64_t R, const void* a, const void* a_scale,
-              const int32_t* offsets, const int32_t* mt, const moe_weights* w, const float* row_gate, void* out,
+int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, bool pair, int64_t R, const void* a,
+              const void* a_scale, const int32_t* offsets, const int32_t* mt, const moe_weights* w, const float* row_gate, void* out,
               void* out_scale, bool raw, int* status, cudaStream_t s) {
   const int E = c->n_experts, S = c->n_shared;
   const uint64_t K = gate_up ? c->hidden : c->inter, N = gate_up ? c->inter : c->hidden;
@@ -350,7 +356,7 @@ int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, int64_t R, c
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   AMaps ma;
-  MxMaps m;
+  MxMaps m{};
   auto weights = [&](CUtensorMap* code, CUtensorMap* scale, const void* cp, const void* sp, uint64_t rows) {
     return map_2d(code, cp, true, K / 2, rows, kStageBytesK, box) && map_u8(scale, sp, K / 32, rows, 16, box);
   };
@@ -363,7 +369,10 @@ int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, int64_t R, c
     if (S) ok = ok && weights(&m.scode1, &m.sscale1, w->sw3, w->ss3, N);
     else m.scode1 = m.code1, m.sscale1 = m.scale1;
   } else {
-    m.code1 = m.code0, m.scale1 = m.scale0, m.scode1 = m.scode0, m.sscale1 = m.sscale0;
+    ok = ok && map_2d(&m.code1, w->w2, true, K / 2, E * N, kStageBytesK, 128) && map_2d(&m.y, out, false, N, R, 64, 32);
+    if (S) ok = ok && map_2d(&m.scode1, w->sw2, true, K / 2, N, kStageBytesK, 128);
+    else m.scode1 = m.code1;
+    m.scale1 = m.scale0, m.sscale1 = m.sscale0;
   }
   if (!ok) return MOE_ERR_CUDA;
   GemmParams g{};
@@ -385,7 +394,7 @@ int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, int64_t R, c
   g.wait_ns = g_wait_ns;
   g.raw_out = raw ? 1 : 0;
   g.inject = g_inject;
-  CUDA_TRY(launch_mxfp4_gemm(g, gate_up, sms, ma, m, s));
+  CUDA_TRY(launch_mxfp4_gemm(g, gate_up, pair, sms, ma, m, s));
   return MOE_OK;
 }
 
@@ -399,7 +408,7 @@ int run_gate_up(const moe_config* c, const WsLayout& L, int64_t R, const void* a
   const bool pair = kind == kPair;
   if (!get_encoder()) return MOE_ERR_CUDA;
   if (c->wdtype == MOE_WDTYPE_MXFP4)
-    return run_mxfp4(c, L, true, R, a, a_scale_t, offsets, mt, w, nullptr, out, out_scale_t, raw, status, s);
+    return run_mxfp4(c, L, true, pair, R, a, a_scale_t, offsets, pair ? mp : mt, w, nullptr, out, out_scale_t, raw, status, s);
   const bool fp8 = c->wdtype == MOE_WDTYPE_FP8_E4M3;
   const int H = c->hidden, I = c->inter, E = c->n_experts, S = c->n_shared;
   const uint32_t box_k = fp8 ? 128 : 64;
@@ -495,7 +504,7 @@ int run_down(const moe_config* c, const WsLayout& L, int64_t R, const void* a, c
   const bool pair = kind == kPair;
   if (!get_encoder()) return MOE_ERR_CUDA;
   if (c->wdtype == MOE_WDTYPE_MXFP4)
-    return run_mxfp4(c, L, false, R, a, a_scale_t, offsets, mt, w, row_gate, y, nullptr, false, status, s);
+    return run_mxfp4(c, L, false, pair, R, a, a_scale_t, offsets, pair ? mp : mt, w, row_gate, y, nullptr, false, status, s);
   const bool fp8 = c->wdtype == MOE_WDTYPE_FP8_E4M3;
   const int H = c->hidden, I = c->inter, E = c->n_experts, S = c->n_shared;
   const uint32_t box_k = fp8 ? 128 : 64;

@@ -201,12 +201,14 @@ cudaError_t launch_nvfp4_gemm(const GemmParams& p, bool gemm1, int grid, const A
 // maps as in NvMaps.
 struct MxMaps {
   CUtensorMap code0, code1, scode0, scode1, scale0, scale1, sscale0, sscale1, a_scale;
+  CUtensorMap y;  // GEMM2 on pairs: y [R, N] bf16 in 32-row x 64-column boxes, 128B swizzle
 };
 
 // MXFP4 grouped GEMM on the block-scaled tensor core: GEMM1 (gate/up + SwiGLU;
 // out = h codes [R, N/2], out_scale = E8M0 bytes [R, N/32]) or GEMM2 (down, bf16
-// y). tm_a maps the activation codes.
-cudaError_t launch_mxfp4_gemm(const GemmParams& p, bool gemm1, int grid, const AMaps& tm_a, const MxMaps& tm,
+// y). tm_a maps the activation codes. pair: 2-SM tiles of 256 rows; p.mt_prefix must
+// then be the pair-tile prefix.
+cudaError_t launch_mxfp4_gemm(const GemmParams& p, bool gemm1, bool pair, int grid, const AMaps& tm_a, const MxMaps& tm,
                               cudaStream_t s);
 
 // Microscaled 4-bit storage (fp4_quantize.cu): n_mat contiguous matrices of

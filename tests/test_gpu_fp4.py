@@ -127,6 +127,14 @@ def test_quantize_non_finite_and_bf16_output(m):
 
 # ------------------------------------------------------------ grouped GEMMs --
 
+@pytest.fixture(params=["single", "pair"])
+def variant(request, m):
+    """The MXFP4 GEMMs on single CTAs, or on pairs of them (same results expected)."""
+    m.moe_set_gemm_variant(m.MOE_GEMM_SINGLE if request.param == "single" else m.MOE_GEMM_PAIR)
+    yield request.param
+    m.moe_set_gemm_variant(m.MOE_GEMM_AUTO)
+
+
 H, I, E = 1024, 512, 5
 COUNTS = [0, 1, 129, 300, 64, 200]  # the shared expert last
 
@@ -153,7 +161,7 @@ def _setup(m):
     return cfg, dev, {n: v for n, (_, _, v) in mats.items()}, offsets, R, np.repeat(np.arange(E + 1), COUNTS), ws
 
 
-def test_mxfp4_gate_up_exact(m):
+def test_mxfp4_gate_up_exact(m, variant):
     import torch
     cfg, dev, w, offsets, R, group, ws = _setup(m)
     ac, asc, a = _matrices(4, 1, R, H)
@@ -169,7 +177,7 @@ def test_mxfp4_gate_up_exact(m):
     assert torch.isnan(out[R]).all()  # nothing behind the last row
 
 
-def test_mxfp4_gate_up_h(m):
+def test_mxfp4_gate_up_h(m, variant):
     """h leaves as MXFP4 of silu(gate) * up: equal to the quantised definition but where a value
     sits on a border of the code grid, within fp32 noise, and there one code apart."""
     import torch
@@ -192,7 +200,7 @@ def test_mxfp4_gate_up_h(m):
     assert np.abs((got & 7) - (want & 7))[same].max() <= 1
 
 
-def test_mxfp4_down_exact(m):
+def test_mxfp4_down_exact(m, variant):
     import torch
     cfg, dev, w, offsets, R, group, ws = _setup(m)
     ac, asc, a = _matrices(5, 1, R, I)
@@ -236,7 +244,7 @@ LAYERS = [(40, 512, 512, 16, 2, 1, False, None), (300, 1024, 512, 24, 4, 1, True
 
 
 @pytest.mark.parametrize("T,H,I,E,k,S,bias,sample", LAYERS)
-def test_mxfp4_layer_parity(m, T, H, I, E, k, S, bias, sample):
+def test_mxfp4_layer_parity(m, T, H, I, E, k, S, bias, sample, variant):
     """Quantise the weights, run the whole layer on them, and compare with the definition."""
     import torch
     wt, w, sh = mx_weights(m, 60 + T, E, S, H, I, bias)
