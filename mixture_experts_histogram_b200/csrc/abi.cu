@@ -29,8 +29,10 @@ int g_gemm_variant = MOE_GEMM_AUTO;
 constexpr int64_t kPairMinRows = 128;
 constexpr int64_t kSwapMinRows = 1;
 constexpr int64_t kSwapMaxRows = 16;
-// MXFP4: both GEMMs on pairs when the routed groups average this many rows.
-constexpr int64_t kMxPairMinRows = 96;
+// MXFP4: both GEMMs on pairs when the routed groups average this many rows, so that
+// many have more than one 128-row tile (352 experts, layer ms on single CTAs and on
+// pairs: 0.81 and 1.03 at 93 rows, 1.16 and 1.11 at 136, 1.35 and 1.20 at 186).
+constexpr int64_t kMxPairMinRows = 128;
 // FP8 down GEMM: staged TMA stores of y when its groups average this many rows
 // and its K (the intermediate size) is at most this deep.
 constexpr int64_t kStoreYMinRows = 128;

@@ -103,12 +103,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
-// Arrive on a barrier of CTA `cta` of the cluster; orders this thread's earlier TMEM
-// stores (waited for and fenced) before the MMA that the leader issues after it.
-__device__ __forceinline__ void arrive_release_cluster(const void* bar, uint32_t cta) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_cta(bar, cta)) : "memory");
-}
-
 template <bool kGemm1, bool kPair, bool kStoreY>
 __global__ void __launch_bounds__(kThreads, 1)
     mxfp4_gemm_kernel(const GemmParams p, const __grid_constant__ AMaps tm_a, const __grid_constant__ MxMaps tm) {
@@ -332,15 +326,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4* src = reinterpret_cast<const uint4*>(sSc + buf * kScBuf) + lane;
 #pragma unroll
         for (int i = 0; i < 12; ++i) sc[i] = src[32 * i];
+        // Both stages' columns, one after the other, then one wait for the stores: waiting
+        // and arriving per stage took longer than a stage's MMAs.
+        const int slot0 = slot;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // The slot is free once the MMAs of its previous use completed.
-          if (!warp_wait<kPair>(&sempty[slot], sf_phase ^ 1, p.status, abort_flag, site0 | 7, item, p.wait_ns)) {
-            ok = false;
-            break;
-          }
+          if (ok) ok = warp_wait<kPair>(&sempty[slot0 + half], sf_phase ^ 1, p.status, abort_flag, site0 | 7, item, p.wait_ns);
           tc_fence_after_sync();
-          const uint32_t col = tmem + lane_base + kSfCol + slot * kSfCols;
+          const uint32_t col = tmem + lane_base + kSfCol + (slot0 + half) * kSfCols;
           uint32_t v[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -354,19 +348,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = half ? sc[4 + i].w : sc[4 + i].y;
           tmem_st8(col + 16, v);
-          if (half == 0) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&scempty[buf]);  // (every lane's values are in registers)
-          }
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (kPair) arrive_release_cluster(&sfull[slot], 0);
-            else mbar_arrive(&sfull[slot]);
-          }
-          if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1; }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scempty[buf]);  // (every lane's values are in registers)
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (kPair) mbar_arrive_cluster(map_to_cta(&sfull[slot0 + half], 0));
+            else mbar_arrive(&sfull[slot0 + half]);
+          }
+        }
+        slot += 2;
+        if (slot == kSfSlots) { slot = 0; sf_phase ^= 1; }
         if (++buf == kScBufs) { buf = 0; sc_phase ^= 1; }
       }
     }
