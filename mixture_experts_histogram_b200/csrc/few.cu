@@ -74,7 +74,7 @@ struct Fmt<MOE_WDTYPE_NVFP4> {
 };
 template <>
 struct Fmt<MOE_WDTYPE_MXFP4> {
-  static constexpr int kPer2 = 4, kSlab = 1024, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 32, kWarps = 8;
+  static constexpr int kPer2 = 4, kSlab = 1024, kScaleSlab = kSlab / 16, kXPad = 64, kBlock = 128, kWarps = 8;
 };
 
 template <int kW>
@@ -159,12 +159,14 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Activations are 16-bit operands: bf16 (BF16); the f16 values of the E4M3 and E2M1
-// codes (FP8, MXFP4; exact); or, for NVFP4, whose activations are not quantised, f16
-// next to a power of two for each 128 inputs that puts the largest at [2^14, 2^15):
-// what f16 cannot hold then is below 2^-39 of that largest one, where the fp32 sums
-// have 24 bits. Values lie in input order, but for NVFP4, whose groups of 8 inputs
-// are transposed 4 x 4 within 32 x 4 inputs, as its lanes read them.
+// Activations are 16-bit operands: bf16 (BF16); the f16 values of the E4M3 codes
+// (FP8; exact); or, for 4-bit weights, f16 next to a power of two for each 128 inputs:
+// NVFP4, whose activations are not quantised, with the largest at [2^14, 2^15); MXFP4,
+// whose quantised values have exponents of their own for each 32 inputs, with the
+// largest of these at 2^12. What f16 cannot hold then is below 2^-36 of the largest
+// value, where the fp32 sums have 24 bits. Values lie in input order, but for NVFP4,
+// whose groups of 8 inputs are transposed 4 x 4 within 32 x 4 inputs, as its lanes
+// read them.
 template <int kW>
 __device__ __forceinline__ int x_group(int v) {
   return kW == MOE_WDTYPE_NVFP4 ? (v & ~15) | (v & 3) << 2 | ((v >> 2) & 3) : v;
@@ -207,7 +209,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // Byte i of a word of E8M0 scales as fp32 (0: 2^-127; 255: infinity, which makes the
 // sums non-finite).
 __device__ __forceinline__ float e8m0_weight(uint32_t word, int i) {
-  return __uint_as_float(max((word << (24 - 8 * i)) >> 24 << 23, 0x00400000u));
+  return __uint_as_float(max(__byte_perm(word, 0, 0x0444u | (uint32_t)i << 12) >> 1, 0x00400000u));
 }
 
 // Sums of a stage, in as many independent chains of MMAs as hide their latency.
@@ -226,17 +228,6 @@ struct Sums {
     return make_float4(s[0], s[1], s[2], s[3]);
   }
 };
-
-// acc += d * s * w: rows g (w0) and g + 8 (w1) of the columns with scales s.
-__device__ __forceinline__ void weigh(float (&acc)[4], const float (&d)[4], float2 s, float w0, float w1) {
-  const float2 z = make_float2(0.0f, 0.0f);
-  const float2 a = fma2(fma2(make_float2(d[0], d[1]), s, z), make_float2(w0, w0), make_float2(acc[0], acc[1]));
-  const float2 b = fma2(fma2(make_float2(d[2], d[3]), s, z), make_float2(w1, w1), make_float2(acc[2], acc[3]));
-  acc[0] = a.x;
-  acc[1] = a.y;
-  acc[2] = b.x;
-  acc[3] = b.y;
-}
 
 // Shared-memory loads by 32-bit address: through generic pointers every one of them
 // would carry 64-bit address arithmetic.
@@ -276,14 +267,13 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
   // The 128-byte swizzle: 16-byte unit i of a line lies at i ^ (line address / 128 % 8).
   const uint32_t x0 = (o.a0 >> 3) & 0x70u, x1 = (o.a1 >> 3) & 0x70u;
   if constexpr (kW == MOE_WDTYPE_MXFP4) {
-    // Eight 32-input blocks, two MMAs each (lane c takes the block's word c); a
-    // block's sum is weighted by both scales.
+    // Eight 32-input blocks, two MMAs each (lane c takes the block's word c); a block's
+    // sum is weighted by the weights' scale, and four blocks' by the activations'.
     const uint32_t a0 = o.a0 + 4 * c, a1 = o.a1 + 4 * c;
     const uint2 w0 = lds64(o.c0), w1 = lds64(o.c1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 s0 = lds128(o.s0 + 16 * h), s1 = lds128(o.s1 + 16 * h);
-      const uint32_t sx0[4] = {s0.x, s0.y, s0.z, s0.w}, sx1[4] = {s1.x, s1.y, s1.z, s1.w};
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const uint32_t u = (uint32_t)(4 * h + b) << 4;
@@ -294,9 +284,17 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         mma_f16(d, va[0], vb[0], va[1], vb[1], x.x, x.y);
         mma_f16(d, va[2], vb[2], va[3], vb[3], x.z, x.w);
-        weigh(acc.a[b & 1], d, make_float2(__uint_as_float(sx0[b]), __uint_as_float(sx1[b])),
-              e8m0_weight(h ? w0.y : w0.x, b), e8m0_weight(h ? w1.y : w1.x, b));
+        const float f0 = e8m0_weight(h ? w0.y : w0.x, b), f1 = e8m0_weight(h ? w1.y : w1.x, b);
+        t[0] = fmaf(d[0], f0, t[0]);
+        t[1] = fmaf(d[1], f0, t[1]);
+        t[2] = fmaf(d[2], f1, t[2]);
+        t[3] = fmaf(d[3], f1, t[3]);
       }
+      const float sx0 = __uint_as_float(lds32(o.s0 + 4 * h)), sx1 = __uint_as_float(lds32(o.s1 + 4 * h));
+      acc.a[h][0] = fmaf(t[0], sx0, acc.a[h][0]);
+      acc.a[h][1] = fmaf(t[1], sx1, acc.a[h][1]);
+      acc.a[h][2] = fmaf(t[2], sx0, acc.a[h][2]);
+      acc.a[h][3] = fmaf(t[3], sx1, acc.a[h][3]);
     }
   } else {
     const uint32_t a0 = o.a0 + ((c << 4) ^ x0), a1 = o.a1 + ((c << 4) ^ x1);
@@ -371,9 +369,16 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
                                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   } else {
     uint32_t m = amax_bits<8>(f);
-    constexpr int kLanes = F::kBlock / 8;  // 16 (FP8, NVFP4) or 4 (MXFP4) lanes share a block
+    constexpr int kLanes = F::kBlock / 8;  // 16 lanes share a block
+    constexpr int kQuantLanes = kW == MOE_WDTYPE_MXFP4 ? 4 : kLanes;
 #pragma unroll
-    for (int o = 1; o < kLanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < kQuantLanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    uint32_t mx_top = 0;  // MXFP4: the largest scale byte of the 128 inputs, blocks of zeros left out
+    if constexpr (kW == MOE_WDTYPE_MXFP4) {
+      mx_top = m ? e8m0_of(m) : 0u;
+#pragma unroll
+      for (int o = 4; o < kLanes; o *= 2) mx_top = max(mx_top, __shfl_xor_sync(0xffffffffu, mx_top, o));
+    }
     if (!live) return;
     float s;
     uint32_t h[4];
@@ -391,7 +396,12 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
     } else if constexpr (kW == MOE_WDTYPE_MXFP4) {
       const uint32_t sb = e8m0_of(m);
       f16_of_e2m1x8(sb == 255u ? 0u : e2m1x8(f, e8m0_rcp(sb)), h);
-      s = e8m0_value(sb);
+      // Code x 2^(sb - mx_top + 12); a non-finite block makes the scale NaN.
+      const int up = (int)min(sb, mx_top) - (int)mx_top + 12;
+      const __half2 r2 = __float2half2_rn(up < -30 ? 0.0f : __uint_as_float((uint32_t)(127 + up) << 23));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = mul_f16x2(h[j], *reinterpret_cast<const uint32_t*>(&r2));
+      s = e8m0_value(mx_top) * 0x1p-12f;
     } else {
       // bf16 values (h is rounded to bf16, as x is) times 2^k, k = 14 - floor(log2(m)); a
       // non-finite or zero block keeps k = 0. 2^k and 2^-k are both normal for eb in [15, 254].
@@ -1297,13 +1307,13 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
   cfg.blockDim = dim3(Smem<kW>::kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  // (Programmatic stream serialization has no effect on a cooperative launch; without
+  // the latter it starts 3 us earlier, but two calls at once could wait for each other.)
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return counted_launch(cudaLaunchKernelEx(&cfg, kern, p, tm));
 }
 
