@@ -26,8 +26,8 @@
 // multiply, each a whole stage in its turn, and two add up their partial sums in
 // stage order and finish the tiles. (With every stage split over the warps the waits
 // and the address arithmetic cost more than the products: 2.0 TB/s for FP8.) The
-// shared expert's rows are known before the routing is: their copies start before
-// the logits are ready.
+// shared expert's rows are known before the routing is: their copies start at once,
+// while the experts are selected.
 // Tensor-core work is mma.sync (m16n8): at 23 weight bytes per clock and SM the
 // MMAs are far from a limit, and 8 columns fit 8 tokens without padding.
 #include <cuda_bf16.h>
@@ -84,6 +84,7 @@ struct Smem {
   static constexpr int kProducers = F::kScaleSlab ? 2 : 1;  // weight rows, scale bytes
   static constexpr int kConsumers = (kWarps + kAcc + kPrep) * 32;
   static constexpr int kThreads = kConsumers + kProducers * 32;
+  static_assert(kMaxRing <= 32 && kHRing <= 32 && kTeams <= 32 && kWarps >= kFewMaxTokens, "one thread per barrier");
   static_assert(kTeams < kHRing, "a team's stages must not skip a whole ring of experts");
   static constexpr int kStageScales = kRows * F::kScaleSlab;  // a stage's scale bytes
   static constexpr int kStage = kRows * F::kSlab + kStageScales;
@@ -379,7 +380,6 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
 #pragma unroll
       for (int o = 4; o < kLanes; o *= 2) mx_top = max(mx_top, __shfl_xor_sync(0xffffffffu, mx_top, o));
     }
-    if (!live) return;
     float s;
     uint32_t h[4];
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
@@ -417,8 +417,8 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
         h[j] = *reinterpret_cast<const uint32_t*>(&v2);
       }
     }
-    *reinterpret_cast<uint4*>(row + x_group<kW>(v) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-    if (v % kLanes == 0) reinterpret_cast<float*>(row + scales_at)[v / kLanes] = s;
+    if (live) *reinterpret_cast<uint4*>(row + x_group<kW>(v) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (live && v % kLanes == 0) reinterpret_cast<float*>(row + scales_at)[v / kLanes] = s;
   }
 }
 
@@ -432,7 +432,6 @@ template <int kW>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewParams p) {
   using L = Smem<kW>;
   pdl_wait();
-  pdl_trigger();  // after the wait: the next kernel may read everything that this one may
   const int router_ctas = (p.E + kRouterExperts - 1) / kRouterExperts;
   if ((int)blockIdx.x >= router_ctas) {
     const int per_row = p.H / 8, v = ((int)blockIdx.x - router_ctas) * kRouterThreads + threadIdx.x;  // 16 k per row
@@ -559,7 +558,7 @@ struct GateUpWalk {
 
 // This CTA's even share of the shared expert, and of the routed ones after it.
 __device__ __forceinline__ int share(const FewParams& p, int experts, int cta) {
-  return (int)((int64_t)experts * (p.I / 8) * cta / gridDim.x);
+  return (int)((uint32_t)(experts * (p.I / 8)) * (uint32_t)cta / gridDim.x);  // below 2^31
 }
 __device__ __forceinline__ GateUpWalk shared_walk(const FewParams& p) {
   return GateUpWalk{share(p, p.S, blockIdx.x), share(p, p.S, blockIdx.x + 1), 0, p.I / 8};
@@ -710,7 +709,7 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
   uint64_t* hempty = hfull + kHRing;     // ... and have been used by all of its stages
   uint64_t* h_ready = hempty + kHRing;   // every CTA's h is written
   uint64_t* x_ready = h_ready + 1;       // x is in shared memory
-  uint64_t* x_done = x_ready + 1;        // ... and has been read for the last time
+  uint64_t* x_done = x_ready + 1;        // ... and has been read for the last time; first[] is complete
   uint64_t* turns = x_done + 1;          // an adding warp's turn to take sums
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
   volatile int* n_list = abort_flag + 1;
@@ -736,25 +735,31 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
   const int h_rows = L::act_bytes(T, H, I) / hpitch;  // rows of h that the activations' space holds, T at least
   const DownRows dr = down_rows(p, i_bytes / kLine);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < n_stages; ++i) {
-      mbar_init(&full[i], kScaleBytes ? 4 : 2);
-      mbar_init(&empty[i], kTeam);
-    }
-    for (int i = 0; i < kTeams; ++i) {
-      mbar_init(&pfull[i], kTeam);
-      mbar_init(&pempty[i], 1);
-    }
-    for (int i = 0; i < kHRing; ++i) {
-      mbar_init(&hfull[i], kPrep);
-      mbar_init(&hempty[i], dr.rows ? dr.groups * dr.slabs * kTeam : 1);
-    }
+  // (One barrier per thread: a single thread's hundred took 0.6 us.)
+  if (warp == 0 && lane < n_stages) {
+    mbar_init(&full[lane], kScaleBytes ? 4 : 2);
+    mbar_init(&empty[lane], kTeam);
+  } else if (warp == 1 && lane < kHRing) {
+    mbar_init(&hfull[lane], kPrep);
+    mbar_init(&hempty[lane], dr.rows ? dr.groups * dr.slabs * kTeam : 1);
+  } else if (warp == 2 && lane < kTeams) {
+    mbar_init(&pfull[lane], kTeam);
+    mbar_init(&pempty[lane], 1);
+  } else if (warp == 3 && lane == 0) {
     mbar_init(h_ready, 1);
     mbar_init(x_ready, 1);
-    mbar_init(x_done, kWarps);
+    mbar_init(x_done, kWarps + 1);
     for (int i = 0; i < kAcc; ++i) mbar_init(&turns[i], 1);
     *abort_flag = 0;
-    fence_mbar_init();
+  }
+  fence_mbar_init();
+  // The logits of the selecting warps, while the rest is set up.
+  constexpr int kPer = kMaxExperts / 32;
+  float logit[kPer];
+  if (warp < T) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      logit[i] = i * 32 + lane < p.E ? __ldcg(p.logits + warp * p.E + i * 32 + lane) : 0.0f;
   }
   for (int i = threadIdx.x; i < 16; i += kThreads) bits[i] = 0;
   for (int i = threadIdx.x; i < kMaxU; i += kThreads) used[i] = 0;
@@ -781,7 +786,6 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
   const int g = lane / 4, c = lane % 4;
   constexpr int kOthers = kConsumers - kUpWarps * 32;  // threads of the selection
   if (warp < kPrep0 || warp >= kPrep0 + kUpWarps) {
-    pdl_wait();  // the logits, x in the operand layout, the cleared counter
     if (threadIdx.x == kConsumers - 32) {  // (a warp without a token to select for)
       mbar_arrive_expect_tx(x_ready, (uint32_t)(T * xpitch));
       bulk_load(act, p.xrows, (uint32_t)(T * xpitch), x_ready);
@@ -789,14 +793,13 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
     if (warp < T) {
       // Top-k of token `warp`: order-preserving integer keys, ties to the lower
       // index, a NaN below everything; a taken expert's key is 0.
-      constexpr int kPer = kMaxExperts / 32;
       uint32_t key[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int e = i * 32 + lane;
         key[i] = 0;
         if (e < p.E) {
-          const uint32_t b = __float_as_uint(__ldcg(p.logits + warp * p.E + e));
+          const uint32_t b = __float_as_uint(logit[i]);
           key[i] = (b & 0x7fffffffu) > 0x7f800000u ? 1u : ((b >> 31) ? ~b : (b | 0x80000000u));
           if (key[i] == 0x7fffffffu) key[i] = 0x80000000u;  // -0 equals +0
         }
@@ -935,9 +938,9 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
       next_scale = fetch_scale(n + A);
       const bool gate_up = n < gu_stages;
       if (!gate_up && x_used) {
+        x_used = false;
         __syncwarp();
         if (lane == 0) mbar_arrive(x_done);
-        x_used = false;
       }
       // The stage's lines, the token rows, and where the weight rows lie: line after line
       // of eight gate rows, and the same of the up rows behind them; or of a group's rows.
@@ -1059,18 +1062,18 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
     // space, entries following entries around it (first[] counts the rows).
     const int me = warp - kWarps - kAcc;
     if (dr.rows == 0) return;  // no rows of the output here
-    if (me == 0 && lane == 0) {
+    if (me == kPrep - 1 && lane == 0) {  // (a warp that loads nothing before)
       int rows = 0;
       for (int i = 0; i < U; ++i) {
         first[i] = rows;
         rows += __popc(used[down_entry(i, U, S)]);
       }
+      mbar_arrive(x_done);
     }
-    named_bar_sync(4, kPrep * 32);
-    if (ok) ok = warp_wait<false>(x_done, 0, p.status, abort_flag, 0x200a, 0, p.wait_ns);
-    if (ok) ok = warp_wait<false>(h_ready, 0, p.status, abort_flag, 0x200b, 0, p.wait_ns);
     // The warps take the rows in turn; a row goes in steps of 96 groups of 8 values,
-    // and a step's values are fetched while the step before is stored.
+    // and a step's values are fetched while the step before is stored. A first turn of
+    // the loop stores nothing: it brings the loop's instructions near while the weights
+    // of the gate/up phase stream (fetched through a busy HBM they took 3 us).
     constexpr int kBatch = 3;
     const int groups = I / 8;
     struct Step {
@@ -1114,18 +1117,21 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
       return o;
     };
     int freed = 0, told = 0;  // entries whose rows are free again, and that this warp has reported
-    Step st = settle(Step{0, down_entry(0, U, S), 0, 0, used[down_entry(0, U, S)]});
+    bool dry = true;
+    Step st{0, 0, 0, 0, 1u};
     Values cur = fetch(st);
 #pragma unroll 1
     while (true) {
-      // Every entry before this step's has this warp's rows.
-      __syncwarp();
-      for (; told < min(st.i, U); ++told)
-        if (lane == 0) mbar_arrive(&hfull[told % kHRing]);
-      if (st.i >= U) break;
-      const Step nx = after(st);
+      if (!dry) {
+        // Every entry before this step's has this warp's rows.
+        __syncwarp();
+        for (; told < min(st.i, U); ++told)
+          if (lane == 0) mbar_arrive(&hfull[told % kHRing]);
+        if (st.i >= U) break;
+      }
+      const Step nx = dry ? st : after(st);
       const Values next = fetch(nx);
-      if (st.j == 0) {
+      if (!dry && st.j == 0) {
         // Room for the row: first[] counts on from entry to entry, the oldest go first.
         const int end = first[st.i] + st.r + 1;
         while (ok && (freed <= st.i - kHRing || first[freed] < end - h_rows)) {
@@ -1134,16 +1140,26 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
           ++freed;
         }
       }
-      uint8_t* row = act + by_rows.rem(first[st.i] + st.r) * hpitch;
+      uint8_t* row = act + (dry ? 0 : by_rows.rem(first[st.i] + st.r)) * hpitch;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int g8 = st.j + 32 * k + lane;
         const float f[8] = {cur.v[2 * k].x,     cur.v[2 * k].y,     cur.v[2 * k].z,     cur.v[2 * k].w,
                             cur.v[2 * k + 1].x, cur.v[2 * k + 1].y, cur.v[2 * k + 1].z, cur.v[2 * k + 1].w};
-        store_operand<kW, false>(row, L::scales_at(I), g8, f, g8 < groups);
+        store_operand<kW, false>(row, L::scales_at(I), g8, f, !dry && g8 < groups);
       }
-      st = nx;
-      cur = next;
+      if (dry) {
+        dry = false;
+        if (ok) ok = warp_wait<false>(x_done, 0, p.status, abort_flag, 0x200a, 0, p.wait_ns);
+        if (ok) ok = warp_wait<false>(h_ready, 0, p.status, abort_flag, 0x200b, 0, p.wait_ns);
+        st.u = down_entry(0, U, S);
+        st.mask = used[st.u];
+        st = ok ? settle(st) : Step{U, 0, 0, 0, 0u};
+        cur = fetch(st);
+      } else {
+        st = nx;
+        cur = next;
+      }
     }
     return;
   }
@@ -1218,11 +1234,10 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
   }
 
   // Grid barrier: every h is written.
-  __threadfence();
   named_bar_sync(3, kAcc * 32);
   if (me == 0 && lane == 0) {
-    __threadfence();
-    atomicAdd(p.counter, 1);
+    // (The release covers the other threads' stores too: they come before the barrier.)
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.counter) : "memory");
     const uint64_t start = global_timer_ns();
     uint32_t spins = 0;
     while (true) {
@@ -1235,7 +1250,6 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
         break;
       }
     }
-    __threadfence();
     mbar_arrive(h_ready);
   }
 
