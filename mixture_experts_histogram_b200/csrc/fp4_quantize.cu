@@ -27,8 +27,11 @@ namespace moe {
 namespace {
 
 constexpr int kVec = 8;       // inputs per thread and step
-constexpr int kUnroll = 4;    // steps whose loads are issued together
 constexpr int kThreads = 256;
+
+// Steps whose loads are issued together: 64 bytes a thread.
+template <typename T>
+constexpr int kSteps = sizeof(T) == 2 ? 4 : 2;
 
 template <typename Tin>
 struct Raw;
@@ -76,7 +79,7 @@ struct NvScale {
     ok = gg > 0.0f && gg < INFINITY;
     r6 = __fdividef(1.0f, 6.0f * gg);
   }
-  __device__ __noinline__ uint32_t scale_slow(float bmax) const {
+  static __device__ __noinline__ uint32_t scale_slow(float bmax, float g) {
     const double q = (double)bmax / (6.0 * (double)g);
     if (q >= 448.0) return 0x7eu;
     int e = q > 0.0 ? ilogb(q) : -6;
@@ -92,17 +95,12 @@ struct NvScale {
     const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q * (1.0f - 0x1p-20f), q * (1.0f + 0x1p-20f)),
                                                   __NV_SATFINITE, __NV_E4M3);
     if ((two & 0xffu) == (two >> 8) && r6 < 0x1p126f && r6 > 0x1p-120f) return two & 0xffu;
-    return scale_slow(b);
+    return scale_slow(b, g);
   }
-  __device__ __noinline__ uint32_t codes_slow(const float (&f)[kVec], float s) const {
-    const double d = (double)s * (double)g;
-    uint32_t w = 0;
-    for (int i = 0; i < kVec; ++i) {
-      const double a = fabs((double)f[i]) / d;
-      const uint32_t c = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
-      w |= (c | (signbit(f[i]) ? 8u : 0u)) << (4 * i);
-    }
-    return w;
+  static __device__ __noinline__ uint32_t code_slow(float f, double d) {
+    const double a = fabs((double)f) / d;
+    const uint32_t c = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
+    return c | (signbit(f) ? 8u : 0u);
   }
   __device__ __forceinline__ uint32_t codes(const float (&f)[kVec], uint32_t sb) const {
     const float s = e4m3_value(sb);
@@ -111,7 +109,10 @@ struct NvScale {
     const float d = s * g, r = __frcp_rn(d);
     const uint32_t lo = e2m1x8(f, r * (1.0f - 0x1p-20f)), hi = e2m1x8(f, r * (1.0f + 0x1p-20f));
     if (lo == hi && d > 0x1p-120f && d < 0x1p120f) return lo;
-    return codes_slow(f, s);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) w |= code_slow(f[i], (double)s * (double)g) << (4 * i);
+    return w;
   }
 };
 
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64
   pdl_wait();
   pdl_trigger();
   constexpr int kLanes = kMx ? 4 : 2;  // lanes of a block
+  constexpr int kUnroll = kSteps<Tin>;
   for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
     const int64_t base = mat * vecs;
     const NvScale nv(kMx ? 1.0f : g[mat]);
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(int64_t n_mat, int64_t v
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t part[kThreads / 32];
+  constexpr int kUnroll = 4;
   for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
     uint32_t m = 0;
     for (int64_t v0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x; v0 < vecs;
@@ -205,6 +208,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(int64_t n_mat, int
   pdl_wait();
   pdl_trigger();
   constexpr int kLanes = kMx ? 4 : 2;
+  constexpr int kUnroll = kSteps<Tout>;
   for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
     const int64_t base = mat * vecs;
     const float gs = kMx ? 1.0f : g[mat];
@@ -281,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) gather_mx_kernel(const GatherParams 
   }
 }
 
-dim3 vec_grid(int64_t n_mat, int64_t vecs) {
-  return dim3((unsigned)ceil_div(vecs, kThreads * kUnroll), (unsigned)(n_mat < 65535 ? n_mat : 65535));
+dim3 vec_grid(int64_t n_mat, int64_t vecs, bool f32) {
+  return dim3((unsigned)ceil_div(vecs, kThreads * (f32 ? kSteps<float> : kSteps<__nv_bfloat16>)), (unsigned)(n_mat < 65535 ? n_mat : 65535));
 }
 
 }  // namespace
@@ -294,7 +298,7 @@ cudaError_t launch_quantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems,
     n_mat = 1;
   }
   const int64_t vecs = elems / kVec;
-  const dim3 grid = vec_grid(n_mat, vecs);
+  const dim3 grid = vec_grid(n_mat, vecs, f32);
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   const float* xf = static_cast<const float*>(x);
@@ -311,7 +315,7 @@ cudaError_t launch_fp4_global_scale(bool f32, int64_t n_mat, int64_t elems, cons
   cudaError_t e = cudaMemsetAsync(g, 0, (size_t)n_mat * 4, s);
   if (e != cudaSuccess) return e;
   const int64_t vecs = elems / kVec;
-  dim3 grid = vec_grid(n_mat, vecs);
+  dim3 grid = vec_grid(n_mat, vecs, f32);
   if (grid.x > 1024) grid.x = 1024;
   uint32_t* gb = reinterpret_cast<uint32_t*>(g);
   e = f32 ? launch_pdl(amax_kernel<float>, grid, dim3(kThreads), 0, s, 1, n_mat, vecs, static_cast<const float*>(x), gb)
@@ -328,7 +332,7 @@ cudaError_t launch_dequantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elem
     n_mat = 1;
   }
   const int64_t vecs = elems / kVec;
-  const dim3 grid = vec_grid(n_mat, vecs);
+  const dim3 grid = vec_grid(n_mat, vecs, f32);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(y);
   float* yf = static_cast<float*>(y);
