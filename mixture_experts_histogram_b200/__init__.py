@@ -122,10 +122,19 @@ def _ptr(t) -> Optional[int]:
     return t.ctypes.data  # numpy
 
 
+_raw_stream = None  # the handle of a device's current stream
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # Without the Stream object that torch.cuda.current_stream() makes (3 us a call).
+            torch.cuda.current_stream()  # raises where there is no device
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -114,3 +114,34 @@ def test_mxfp4_layer_refusals(lib):
                                           (m.MOE_STAGE_DOWN, 4096 + 8, None, m.MOE_ERR_MISALIGNED)):
         assert g(ctypes.byref(cfg), stage, 4, *args, a_scale, ctypes.byref(w), None, 8192, out_scale, 16384, 1 << 30,
                  None) == rc
+
+
+def test_few_refusals(lib):
+    cfg = m.make_config(1024, 16, 2, 1, 512, m.MOE_WDTYPE_FP8_E4M3)
+    fake = {k: 1 << 20 for k in m.WEIGHT_FIELDS}
+    w = m.moe_weights(*[fake[k] for k in m.WEIGHT_FIELDS])
+
+    def call(T=4, x=1024, out=2048, idx=None, gate=None, ws=4096, nb=1 << 30, cfg=cfg, w=w):
+        return lib.moe_forward_few(ctypes.byref(cfg), T, x, ctypes.byref(w), out, idx, gate, ws, nb, None)
+    assert call(nb=16) == m.MOE_ERR_WORKSPACE_TOO_SMALL            # everything else is in order
+    assert call(T=0) == m.MOE_OK                                   # nothing to do
+    assert call(T=m.MOE_FEW_MAX_TOKENS + 1) == m.MOE_ERR_UNSUPPORTED_SHAPE
+    assert call(T=-1) == call(x=None) == call(out=None) == call(ws=None) == m.MOE_ERR_INVALID_ARG
+    assert call(idx=8192) == call(gate=8192) == m.MOE_ERR_INVALID_ARG
+    assert call(x=1032) == call(out=2056) == call(ws=4096 + 64) == m.MOE_ERR_MISALIGNED
+    assert call(w=m.moe_weights(*[None if k == "s2" else fake[k] for k in m.WEIGHT_FIELDS])) == m.MOE_ERR_INVALID_ARG
+    # Activations that leave no room for the weights: T * max(H, I) beyond 65,536 by enough.
+    for wdtype in range(4):
+        for H, I in ((16384, 512), (512, 16384)):
+            big = m.make_config(H, 16, 2, 1, I, wdtype)
+            assert call(T=8, cfg=big) == m.MOE_ERR_UNSUPPORTED_SHAPE
+            assert call(T=4, cfg=big, nb=16) == m.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert call(cfg=m.make_config(1024, 16, 17, 1, 512, 0)) == m.MOE_ERR_UNSUPPORTED_SHAPE
+
+
+def test_few_workspace(lib):
+    """The few-token layer's scratch is part of every workspace that it may be called with."""
+    cfg = m.make_config(4096, 352, 8, 1, 1536, m.MOE_WDTYPE_FP8_E4M3)
+    sizes = [m.moe_workspace_bytes(cfg, T) for T in range(1, 10)]
+    assert all(a < b for a, b in zip(sizes[:8], sizes[1:8]))
+    assert sizes[7] > 65 * 8 * 1536 * 4  # h of (8 x 8 + 1) experts in fp32

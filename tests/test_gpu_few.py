@@ -96,7 +96,8 @@ def bits(t):
 # T, H, I, E, k, S, bias
 SHAPES = [(1, 512, 512, 4, 1, 1, False), (2, 1024, 512, 40, 8, 1, False), (8, 512, 1024, 24, 3, 0, True),
           (3, 512, 512, 5, 5, 1, False), (8, 4096, 1536, 16, 8, 1, False), (5, 512, 512, 512, 16, 1, False), (6, 2560, 512, 20, 4, 1, False),
-          (7, 512, 512, 1, 1, 0, False)]
+          (7, 512, 512, 1, 1, 0, False), (8, 512, 512, 200, 16, 1, False), (8, 8192, 512, 2, 1, 1, False),
+          (8, 512, 8192, 2, 1, 0, False), (1, 16384, 512, 3, 2, 1, False), (1, 1024, 13824, 1, 1, 0, False)]
 SMALL = [(1, 128, 128, 4, 2, 1, False), (8, 384, 640, 9, 2, 1, False), (6, 256, 256, 300, 4, 0, True)]
 
 

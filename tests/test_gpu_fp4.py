@@ -268,3 +268,105 @@ def test_mxfp4_layer_parity(m, T, H, I, E, k, S, bias, sample, variant):
     err, per = frob_rel(got, want), rows_rel(got, want)
     print(f"T={T}: rel Frobenius {err:.2e}, per-token max {per.max():.2e}")
     assert err < 1e-2 and per.max() < 1e-2
+
+
+def test_mxfp4_nan_tokens_stay_alone(m, variant):
+    """A token with a NaN or an infinity gives non-finite rows; the others keep their bits."""
+    import torch
+    T, H, I, E, k = 50, 512, 512, 6, 2
+    wt, _, _ = mx_weights(m, 70, E, 1, H, I)
+    cfg = m.make_config(H, E, k, 1, I, m.MOE_WDTYPE_MXFP4)
+    ws = torch.empty(m.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    x = m.to_device(synth.normal_bf16(71, 1, (T, H), 1.0))
+    idx = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:k] for t in range(T)]).int().cuda()
+    gate = torch.full((T, k), 0.5, device="cuda")
+    outs = []
+    for bad in (False, True):
+        xb = x.clone()
+        if bad:
+            xb[3, 5], xb[20, 511] = float("nan"), float("-inf")
+        y = torch.empty((3 * T, H), dtype=torch.bfloat16, device="cuda")
+        pos = torch.empty((T, 3), dtype=torch.int32, device="cuda")
+        out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        m.moe_experts(cfg, T, xb, idx, gate, m.make_weights(wt), y, pos, ws)
+        m.moe_combine(cfg, T, y, pos, out)
+        assert m.moe_read_status(ws) == 0
+        outs.append(out.float())
+    keep = [t for t in range(T) if t not in (3, 20)]
+    assert torch.equal(outs[0][keep], outs[1][keep])
+    assert not torch.isfinite(outs[1][[3, 20]]).any()
+
+
+def test_mxfp4_run_together(m):
+    """Quantise, route, experts and combine, the whole forward, the expert-parallel shares, and the
+    few-token layer: one layer, and what each entry point gives for it."""
+    import torch
+    T, H, I, E, k = 8, 1024, 512, 16, 4
+    wt, _, _ = mx_weights(m, 72, E, 1, H, I)
+    cfg = m.make_config(H, E, k, 1, I, m.MOE_WDTYPE_MXFP4)
+    ws = torch.empty(m.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    x = m.to_device(synth.normal_bf16(73, 1, (T, H), 1.0))
+    w = m.make_weights(wt)
+    new = lambda *s, d=torch.bfloat16: torch.empty(s, dtype=d, device="cuda")
+    whole, staged, few, ep = (new(T, H) for _ in range(4))
+    m.moe_forward(cfg, T, x, w, whole, ws)
+    idx, gate = new(T, k, d=torch.int32), new(T, k, d=torch.float32)
+    m.moe_route(cfg, T, x, wt["router_w"], None, idx, gate, None, ws)
+    y, pos = new(5 * T, H), new(T, 5, d=torch.int32)
+    m.moe_experts(cfg, T, x, idx, gate, w, y, pos, ws)
+    m.moe_combine(cfg, T, y, pos, staged)
+    assert torch.equal(whole, staged)
+    m.moe_forward_few(cfg, T, x, w, few, ws)
+    # Both round bf16 outputs (2^-8 at most each); moe_forward rounds each of the five rows before that.
+    err = (few.double() - whole.double()).norm() / whole.double().norm()
+    assert err < 1e-2, err
+    parts = []
+    for e0, e1, t0, t1 in ((0, 6, 0, 3), (6, 16, 3, T)):
+        mine = {n: (v[e0:e1].contiguous() if n in ("w1", "w3", "w2", "s1", "s3", "s2") else v) for n, v in wt.items()}
+        part = new(T, H, d=torch.float32)
+        m.moe_forward_ep_partial(cfg, T, x, m.make_weights(mine), e0, e1, t0, t1, part, ws)
+        assert m.moe_read_status(ws) == 0
+        parts.append((part, mine))
+    m.moe_ep_reduce([p for p, _ in parts], T, H, 0, T, ep)
+    # The same bf16 rows added in another order in fp32, then one rounding: a bf16 step apart at most.
+    assert ((ep.double() - whole.double()).abs() <= 2.0 ** -7 * whole.double().abs() + 1e-6).all()
+
+
+def test_mxfp4_wait_runs_out(m, variant):
+    """With no loads issued every wait ends: a timeout is latched and the device stays usable."""
+    import torch
+    T, H, I, E, k = 16, 512, 512, 4, 2
+    wt, _, _ = mx_weights(m, 74, E, 0, H, I)
+    cfg = m.make_config(H, E, k, 0, I, m.MOE_WDTYPE_MXFP4)
+    ws = torch.empty(m.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    x = m.to_device(synth.normal_bf16(75, 1, (T, H), 1.0))
+    first, again = (torch.empty((T, H), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m.moe_forward(cfg, T, x, m.make_weights(wt), first, ws)
+    m.moe_debug_inject(m.MOE_INJECT_GEMM_NO_LOADS, 50_000_000)
+    try:
+        m.moe_forward(cfg, T, x, m.make_weights(wt), again, ws)
+        assert m.moe_read_status(ws) == m.MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        m.moe_debug_inject(m.MOE_INJECT_NONE, 0)
+    m.moe_forward(cfg, T, x, m.make_weights(wt), again, ws)
+    assert m.moe_read_status(ws) == 0 and torch.equal(first, again)
+
+
+def test_quantize_beyond_32_bits(m):
+    """More than 2^32 values: the last blocks are where they belong."""
+    import torch
+    n, rows, k = 3, 350_000, 4096
+    x = torch.zeros((n, rows, k), dtype=torch.bfloat16, device="cuda")
+    x[-1, -1] = torch.arange(k, device="cuda") % 7 - 3
+    codes = torch.empty((n, rows, k // 2), dtype=torch.uint8, device="cuda")
+    for fmt, blk in ((m.MOE_WDTYPE_MXFP4, 32), (m.MOE_WDTYPE_NVFP4, 16)):
+        g = None if blk == 32 else torch.ones(n, device="cuda")
+        scales = torch.empty((n, rows, k // blk), dtype=torch.uint8, device="cuda")
+        m.moe_quantize_fp4(fmt, n, rows, k, x, g, codes, scales)
+        last = x[-1:, -1:].float().cpu().numpy()
+        c, s = ref.mx_quantize(last) if blk == 32 else ref.nv_quantize(last, [1.0])
+        assert np.array_equal(codes[-1, -1].cpu().numpy(), c[0, 0]) and np.array_equal(scales[-1, -1].cpu().numpy(), s[0, 0])
+        assert not codes[-1, -2].any() and not codes[0, 0].any()
+        y = torch.empty_like(x)
+        m.moe_dequantize_fp4(fmt, n, rows, k, codes, scales, g, y)
+        assert torch.equal(y, x)
