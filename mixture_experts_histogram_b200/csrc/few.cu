@@ -207,10 +207,19 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Byte i of a word of E8M0 scales as fp32 (0: 2^-127; 255: infinity, which makes the
-// sums non-finite).
-__device__ __forceinline__ float e8m0_weight(uint32_t word, int i) {
-  return __uint_as_float(max(__byte_perm(word, 0, 0x0444u | (uint32_t)i << 12) >> 1, 0x00400000u));
+// The four E8M0 scales of a word as fp32 (by way of bf16, which holds them all; 255: NaN).
+__device__ __forceinline__ void e8m0_weights(uint32_t word, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(word));
+  f[0] = __uint_as_float(lo << 16);
+  f[1] = __uint_as_float(lo & 0xffff0000u);
+  f[2] = __uint_as_float(hi << 16);
+  f[3] = __uint_as_float(hi & 0xffff0000u);
 }
 
 // Sums of a stage, in as many independent chains of MMAs as hide their latency.
@@ -274,7 +283,9 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
     const uint2 w0 = lds64(o.c0), w1 = lds64(o.c1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      float t[4] = {0.f, 0.f, 0.f, 0.f}, f0[4], f1[4];
+      e8m0_weights(h ? w0.y : w0.x, f0);
+      e8m0_weights(h ? w1.y : w1.x, f1);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const uint32_t u = (uint32_t)(4 * h + b) << 4;
@@ -285,11 +296,10 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         mma_f16(d, va[0], vb[0], va[1], vb[1], x.x, x.y);
         mma_f16(d, va[2], vb[2], va[3], vb[3], x.z, x.w);
-        const float f0 = e8m0_weight(h ? w0.y : w0.x, b), f1 = e8m0_weight(h ? w1.y : w1.x, b);
-        t[0] = fmaf(d[0], f0, t[0]);
-        t[1] = fmaf(d[1], f0, t[1]);
-        t[2] = fmaf(d[2], f1, t[2]);
-        t[3] = fmaf(d[3], f1, t[3]);
+        t[0] = fmaf(d[0], f0[b], t[0]);
+        t[1] = fmaf(d[1], f0[b], t[1]);
+        t[2] = fmaf(d[2], f1[b], t[2]);
+        t[3] = fmaf(d[3], f1[b], t[3]);
       }
       const float sx0 = __uint_as_float(lds32(o.s0 + 4 * h)), sx1 = __uint_as_float(lds32(o.s1 + 4 * h));
       acc.a[h][0] = fmaf(t[0], sx0, acc.a[h][0]);

@@ -39,6 +39,7 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_kept(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void get(float (&f)[kVec]) const {
     const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
@@ -55,6 +56,10 @@ struct Raw<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_kept(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void get(float (&f)[kVec]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -116,7 +121,9 @@ struct NvScale {
   }
 };
 
-// Grid: x over a matrix's vectors, y over matrices (MXFP4 ignores matrix borders: y = 1).
+// Grid: x over a matrix's vectors, y over matrices (MXFP4 ignores matrix borders: y = 1),
+// both taken from the end: what a pass over x before this one (the global scale's) left
+// in L2 is its end, and the inverse, from the front, finds the codes written last.
 template <bool kMx, typename Tin>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64_t vecs, const Tin* __restrict__ x,
                                                             const float* __restrict__ g, uint32_t* __restrict__ codes,
@@ -125,10 +132,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64
   pdl_trigger();
   constexpr int kLanes = kMx ? 4 : 2;  // lanes of a block
   constexpr int kUnroll = kSteps<Tin>;
-  for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
+  for (int64_t mat = n_mat - 1 - blockIdx.y; mat >= 0; mat -= gridDim.y) {
     const int64_t base = mat * vecs;
     const NvScale nv(kMx ? 1.0f : g[mat]);
-    const int64_t v0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+    const int64_t v0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
     Raw<Tin> raw[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(int64_t n_mat, int64_t v
       Raw<Tin> raw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (v0 + u * kThreads < vecs) raw[u].load(x + (mat * vecs + v0 + u * kThreads) * kVec);
+        if (v0 + u * kThreads < vecs) raw[u].load_kept(x + (mat * vecs + v0 + u * kThreads) * kVec);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (v0 + u * kThreads >= vecs) break;
@@ -200,6 +207,8 @@ __global__ void __launch_bounds__(kThreads) global_scale_kernel(int64_t n_mat, f
   if (i < n_mat) g[i] = g[i] == 0.0f ? 1.0f : __fdiv_rn(g[i], 2688.0f);
 }
 
+// A thread writes 16 bytes a step, so that a warp's stores are whole lines: 8 bf16 values,
+// or 4 fp32 ones (half a word of codes; two 16-byte stores of a word's 8 were 10% slower).
 template <bool kMx, typename Tout>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(int64_t n_mat, int64_t vecs,
                                                               const uint32_t* __restrict__ codes,
@@ -207,44 +216,46 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(int64_t n_mat, int
                                                               const float* __restrict__ g, Tout* __restrict__ y) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kLanes = kMx ? 4 : 2;
-  constexpr int kUnroll = kSteps<Tout>;
+  constexpr int kOut = 16 / sizeof(Tout), kParts = kVec / kOut;  // values of a step, steps of a word
+  constexpr int kLanes = (kMx ? 4 : 2) * kParts;                 // steps of a block
+  constexpr int kUnroll = 4;
+  const int64_t steps = vecs * kParts;
   for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
-    const int64_t base = mat * vecs;
+    const int64_t base = mat * steps;
     const float gs = kMx ? 1.0f : g[mat];
     const int64_t v0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
     uint32_t w[kUnroll], sb[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t v = v0 + u * kThreads;
-      if (v < vecs) {
-        w[u] = __ldcs(codes + base + v);
+      if (v < steps) {
+        w[u] = __ldcs(codes + (base + v) / kParts);
         sb[u] = scales[(base + v) / kLanes];
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t v = v0 + u * kThreads;
-      if (v >= vecs) break;
+      if (v >= steps) break;
+      if (kParts == 2) w[u] >>= 16 * (v & 1);  // (a matrix is whole words)
       // Value = (code x block scale) x global scale: the first product is exact.
       const float s = kMx ? e8m0_value(sb[u]) : e4m3_value(sb[u]);
-      float f[kVec];
+      float f[kOut];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
+      for (int i = 0; i < kOut; ++i) {
         // E2M1 as fp32: exponent and mantissa bits in place, then rescaled by 2^126 (exact, zero and 0.5 included).
         const uint32_t c = w[u] >> (4 * i);
         const float e = __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
         f[i] = kMx ? e * s : __fmul_rn(__fmul_rn(e, s), gs);
       }
-      if constexpr (sizeof(Tout) == 2) {
+      if constexpr (kOut == 8) {
         uint4 o;
         __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(&o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) ob[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         __stcs(reinterpret_cast<uint4*>(y) + base + v, o);
       } else {
-        __stcs(reinterpret_cast<float4*>(y) + 2 * (base + v), make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(reinterpret_cast<float4*>(y) + 2 * (base + v) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        __stcs(reinterpret_cast<float4*>(y) + base + v, make_float4(f[0], f[1], f[2], f[3]));
       }
     }
   }
@@ -285,8 +296,12 @@ __global__ void __launch_bounds__(kThreads) gather_mx_kernel(const GatherParams 
   }
 }
 
+// CTAs for n_mat matrices of `steps` steps, `unroll` a thread.
+dim3 step_grid(int64_t n_mat, int64_t steps, int unroll) {
+  return dim3((unsigned)ceil_div(steps, kThreads * unroll), (unsigned)(n_mat < 65535 ? n_mat : 65535));
+}
 dim3 vec_grid(int64_t n_mat, int64_t vecs, bool f32) {
-  return dim3((unsigned)ceil_div(vecs, kThreads * (f32 ? kSteps<float> : kSteps<__nv_bfloat16>)), (unsigned)(n_mat < 65535 ? n_mat : 65535));
+  return step_grid(n_mat, vecs, f32 ? kSteps<float> : kSteps<__nv_bfloat16>);
 }
 
 }  // namespace
@@ -332,7 +347,7 @@ cudaError_t launch_dequantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elem
     n_mat = 1;
   }
   const int64_t vecs = elems / kVec;
-  const dim3 grid = vec_grid(n_mat, vecs, f32);
+  const dim3 grid = step_grid(n_mat, f32 ? 2 * vecs : vecs, 4);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(y);
   float* yf = static_cast<float*>(y);
