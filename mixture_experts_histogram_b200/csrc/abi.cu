@@ -363,6 +363,7 @@ int run_mxfp4(const moe_config* c, const WsLayout& L, bool gate_up, bool pair, i
     return map_2d(code, cp, true, K / 2, rows, kStageBytesK, box) && map_u8(scale, sp, K / 32, rows, 16, box);
   };
   bool ok = amaps(&ma, a, true, K / 2, R) && map_u8(&m.a_scale, a_scale, K / 32, R, 16, kTileM) &&
+            map_2d(&m.a8, a, true, K / 2, R, kStageBytesK, 8) && map_u8(&m.a_scale8, a_scale, K / 32, R, 16, 8) &&
             weights(&m.code0, &m.scale0, gate_up ? w->w1 : w->w2, gate_up ? w->s1 : w->s2, E * N);
   if (S) ok = ok && weights(&m.scode0, &m.sscale0, gate_up ? w->sw1 : w->sw2, gate_up ? w->ss1 : w->ss2, N);
   else m.scode0 = m.code0, m.sscale0 = m.scale0;

@@ -198,9 +198,10 @@ cudaError_t launch_nvfp4_gemm(const GemmParams& p, bool gemm1, int grid, const A
 // MXFP4 maps of one grouped GEMM (uint8): E2M1 codes [rows, K/2] with 128-byte
 // boxes (128B swizzle, one 256-deep K stage) and E8M0 scales [rows, K/32] with
 // 16-byte boxes (two stages), activations' scales in 128-row boxes; the weight
-// maps as in NvMaps.
+// maps as in NvMaps. a8, a_scale8: activation codes and scales of up to 8 rows
+// (decode tiles).
 struct MxMaps {
-  CUtensorMap code0, code1, scode0, scode1, scale0, scale1, sscale0, sscale1, a_scale;
+  CUtensorMap code0, code1, scode0, scode1, scale0, scale1, sscale0, sscale1, a_scale, a8, a_scale8;
   CUtensorMap y;  // GEMM2 on pairs: y [R, N] bf16 in 32-row x 64-column boxes, 128B swizzle
 };
 

@@ -15,7 +15,9 @@
 // scales and inputs are flat arrays of blocks: one thread takes 8 inputs (16 or
 // 32 bytes in, 4 bytes out) and 4 (MXFP4) or 2 (NVFP4) neighbouring lanes share
 // a block. Bound by HBM: 2 (bf16) or 4 (fp32) bytes in and 0.53 / 0.56 out per
-// input.
+// input. Measured: 44 x 1536 x 4096 bf16 to MXFP4 139 us (700 MB, 5.0 TB/s) and back
+// 108 us (6.5 TB/s); 24 x 1001 x 1536 fp32 to NVFP4 and back, the global scale's pass
+// included, 84 us (484 MB, 5.8 TB/s).
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -14,6 +14,11 @@
 // shared memory moves 128 bytes a clock: single CTAs write 51 KB and read 48 KB of it
 // for 512 clocks of MMA, a pair's CTA 35 KB and 32 KB.
 //
+// A tile loads the smallest box that covers its group's rows (8, 32, 64 or 128); the other
+// rows of the MMA are zeros or an earlier tile's, and their results are not stored. Under
+// the power limit, where decode batches run, boxes from 8 rows and zeroed buffers take
+// 64 tokens on 352 experts from 528 to 490 us (at 32 rows and more, with what lay there).
+//
 // Operand tiles come by TMA (128B swizzle) and so do the scales, as row-major 16-byte
 // boxes that cover two stages. The tensor core reads scales from TMEM, four bytes (128
 // inputs) per 32-bit column, row r in lane r % 32 and column r / 32, repeated in the
@@ -25,6 +30,12 @@
 // buffer's shared columns first and then lets the next tile's MMAs begin.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 scale writers, 6..13 epilogue.
+//
+// Measured (H = 4096, I = 1536): 16 tokens on 88 experts, single CTAs: gate/up 82 us, 468
+// MB at 68% of DRAM peak, the weight stream. 8192 tokens on 352 experts, pairs: gate/up 625
+// us (3.0 PFLOP/s) and down 390 us (2.4); loads alone, without MMAs and epilogue, take 462
+// and 358 us, so the tiles' way from L2 bounds the second and most of the first (the
+// layer on single CTAs: 1.35 ms, on pairs 1.20).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -168,6 +179,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
+  // Rows that no box has filled yet multiply as zeros, which draws less power than what
+  // an earlier kernel left there.
+  for (int i = threadIdx.x; i < C::kStages * kABytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(sA)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   __syncthreads();
   if (kPair) cluster_sync();  // the peer's barriers are initialised before any remote arrive
   tc_fence_after_sync();
@@ -202,9 +218,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* f0 = shared ? &tm.sscale0 : &tm.scale0;
         const CUtensorMap* f1 = shared ? &tm.sscale1 : &tm.scale1;
         const int my_row0 = it.row0 + my_off;
-        auto a_rows = [&](int row0) { const int v = it.end - row0; return v <= 32 ? 32 : (v <= 64 ? 64 : 128); };
+        auto a_rows = [&](int row0) {
+          const int v = it.end - row0;
+          return v <= 8 ? 8 : v <= 32 ? 32 : v <= 64 ? 64 : 128;
+        };
         const int my_a = a_rows(my_row0);
-        const CUtensorMap* amap = my_a == 32 ? &tm_a.rows32 : (my_a == 64 ? &tm_a.rows64 : &tm_a.rows128);
+        const CUtensorMap* amap =
+            my_a == 8 ? &tm.a8 : my_a == 32 ? &tm_a.rows32 : (my_a == 64 ? &tm_a.rows64 : &tm_a.rows128);
+        const CUtensorMap* smap = my_a == 8 ? &tm.a_scale8 : &tm.a_scale;
+        const uint32_t sc_tx = my_a == 8 ? kScBuf - (kTileM - 8) * 16 : kScBuf;
         const uint32_t tx = kPair ? (uint32_t)(a_rows(it.row0) + a_rows(it.row0 + kTileM)) * kStageBytesK + 2u * C::kBBytes
                                   : (uint32_t)my_a * kStageBytesK + C::kBBytes;
         for (int ks = 0; ks < kstages; ++ks) {
@@ -215,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint8_t* sc = sSc + buf * kScBuf;
             const int kx = ks * (kStageK / 32);
-            mbar_arrive_expect_tx(&scfull[buf], kScBuf);
-            tma_load_2d(sc, &tm.a_scale, &scfull[buf], kx, my_row0);
+            mbar_arrive_expect_tx(&scfull[buf], sc_tx);
+            tma_load_2d(sc, smap, &scfull[buf], kx, my_row0);
             tma_load_2d(sc + kTileM * 16, f0, &scfull[buf], kx, yb);
             if (kGemm1) tma_load_2d(sc + 2 * kTileM * 16, f1, &scfull[buf], kx, yb);
             sc_issued |= 1u << buf;
