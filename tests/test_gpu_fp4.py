@@ -332,6 +332,41 @@ def test_mxfp4_run_together(m):
     assert ((ep.double() - whole.double()).abs() <= 2.0 ** -7 * whole.double().abs() + 1e-6).all()
 
 
+def test_mxfp4_from_host_and_replayed(m, variant):
+    """The host-buffer entry points, and a graph of the forward replayed on other inputs, give the
+    device call's bytes."""
+    import torch
+    T, H, I, E, k = 200, 1024, 512, 3, 2
+    wt, _, _ = mx_weights(m, 81, E, 1, H, I)
+    cfg = m.make_config(H, E, k, 1, I, m.MOE_WDTYPE_MXFP4)
+    w = m.make_weights(wt)
+    ws = torch.empty(m.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    xs = [m.to_device(synth.normal_bf16(82 + i, 1, (T, H), 1.0)) for i in range(2)]
+    want = []
+    for x in xs:
+        want.append(torch.empty(T, H, dtype=torch.bfloat16, device="cuda"))
+        m.moe_forward(cfg, T, x, w, want[-1], ws)
+    torch.cuda.synchronize()
+    back = torch.zeros(T, H, dtype=torch.bfloat16).pin_memory()
+    hosts = [x.cpu().pin_memory() for x in xs]
+    m.moe_forward_host(cfg, T, hosts[0], w, back, ws)
+    assert torch.equal(back.view(torch.int16), want[0].cpu().view(torch.int16))
+    m.moe_forward_host_async(cfg, T, hosts[1], w, back, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(back.view(torch.int16), want[1].cpu().view(torch.int16))
+    x, out = xs[0].clone(), torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            m.moe_forward(cfg, T, x, w, out, ws)
+        for i in (1, 0):
+            x.copy_(xs[i])
+            g.replay()
+            side.synchronize()
+            assert torch.equal(out.view(torch.int16), want[i].view(torch.int16))
+
+
 def test_mxfp4_wait_runs_out(m, variant):
     """With no loads issued every wait ends: a timeout is latched and the device stays usable."""
     import torch
