@@ -95,8 +95,8 @@ typedef struct moe_config {
 } moe_config;
 
 /* Device pointers to one layer's weights (see the layouts above). Scale
- * pointers are used for every storage but MOE_WDTYPE_BF16; shared-expert pointers only when n_shared == 1. router_bias may be NULL (no
- * bias).
+ * pointers are used for every storage but MOE_WDTYPE_BF16; shared-expert
+ * pointers only when n_shared == 1. router_bias may be NULL (no bias).
  * MOE_WDTYPE_NVFP4 (TensorFold PR page: the NVFP4 format its W4A16 linears
  * read; a variant the pages describe for another model): every expert matrix
  * [n, k] is stored as E2M1 codes [n, k/2] uint8, two per byte with input 2j in
@@ -159,9 +159,8 @@ MOE_API int moe_forward(const moe_config* cfg, int64_t T, const void* x, const m
  * ascending index and the shared expert last: a token's result does not depend on
  * the other tokens of the call. The tokens' activations must leave room for the
  * weight ring in shared memory (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * max(H, I)
- * <= 65,536 always does. Needs a device that
- * supports cooperative launches with the whole GPU free for them (no other
- * kernel may hold its SMs forever). One workspace serves one call at a time.
+ * <= 65,536 always does. The cooperative launch starts when every SM is free: it
+ * waits for kernels of other streams to end. One workspace serves one call at a time.
  */
 enum { MOE_FEW_MAX_TOKENS = 8 };
 MOE_API int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w, void* out,
@@ -400,7 +399,9 @@ MOE_API const char* moe_profile_kernel_name(int i);
  * n_experts <= top_k * T <= 16 * n_experts and both NVFP4 GEMMs swapped when
  * top_k * T <= 16 * n_experts, else the gate/up GEMM on pairs when
  * top_k * T >= 128 * n_experts (routed groups of 128+ rows on average) and
- * everything else on single CTAs. The stage entry point applies the same rules
+ * everything else on single CTAs. MXFP4: AUTO runs both GEMMs on pairs when
+ * top_k * T >= 128 * n_experts, else on single CTAs; PAIR both on pairs, SWAP as
+ * SINGLE. The stage entry point applies the same rules
  * with its R rows and n_experts + n_shared groups. All variants compute the
  * same layer and are held to the same tolerance by the tests. */
 enum { MOE_GEMM_AUTO = 0, MOE_GEMM_SINGLE = 1, MOE_GEMM_PAIR = 2, MOE_GEMM_SWAP = 3 };

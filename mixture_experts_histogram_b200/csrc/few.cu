@@ -32,12 +32,13 @@
 // Tensor-core work is mma.sync (m16n8): at 23 weight bytes per clock and SM the
 // MMAs are far from a limit, and 8 columns fit 8 tokens without padding.
 //
-// Measured (H = 4096, I = 1536, 352 experts, top-8 and a shared one; the weights' share
-// of 6.45 TB/s): BF16 T = 3 155 us (0.92), FP8 T = 8 215-228 us (0.8), T = 1 47-49 us
-// (0.55: of these the logits, the cooperative launch and the selection take 8 us, the
+// Measured (H = 4096, I = 1536, 352 experts, top-8 and a shared one, in long runs under
+// the power limit; the floor is the weights at 6.45 TB/s): BF16 T = 3 159 us (0.91 of the
+// floor's rate), FP8 T = 8 234 us (0.75; 212 us in short runs at full clocks), T = 1 47 us
+// (0.57: of these the logits, the cooperative launch and the selection take 8 us, the
 // first tile 3 and the barrier 4). 4-bit storage is bound by the expansion of the codes,
-// about 390 warp instructions for a 2 KB line of 16 rows: MXFP4 T = 8 216 us (0.44), T = 1
-// 51 us; NVFP4 T = 5 143-153 us (0.43). Twelve multiplying warps instead of eight leave 96
+// about 370 warp instructions for a 2 KB line of 16 rows: MXFP4 T = 8 216 us (0.44), T = 1
+// 49 us; NVFP4 T = 5 149 us (0.44). Twelve multiplying warps instead of eight leave 96
 // registers each: MXFP4 T = 8 242 us; the halves of a line as a rolled loop: 230 us, two
 // lines unrolled: 288 us.
 #include <cuda_bf16.h>

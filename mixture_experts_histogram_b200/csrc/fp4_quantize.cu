@@ -15,9 +15,9 @@
 // scales and inputs are flat arrays of blocks: one thread takes 8 inputs (16 or
 // 32 bytes in, 4 bytes out) and 4 (MXFP4) or 2 (NVFP4) neighbouring lanes share
 // a block. Bound by HBM: 2 (bf16) or 4 (fp32) bytes in and 0.53 / 0.56 out per
-// input. Measured: 44 x 1536 x 4096 bf16 to MXFP4 139 us (700 MB, 5.0 TB/s) and back
-// 108 us (6.5 TB/s); 24 x 1001 x 1536 fp32 to NVFP4 and back, the global scale's pass
-// included, 84 us (484 MB, 5.8 TB/s).
+// input. Measured, 44 x 1536 x 4096 values: bf16 to MXFP4 118 us (700 MB, 5.9 TB/s) and
+// back 104 us (6.7), fp32 to MXFP4 183 us (6.8); to NVFP4, where the arithmetic bounds it,
+// bf16 235 us (3.0), fp32 207 to 218 us (6); the NVFP4 global scale 82 us bf16, 157 us fp32.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -29,11 +29,16 @@ namespace moe {
 namespace {
 
 constexpr int kVec = 8;       // inputs per thread and step
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kGatherThreads = 256;
 
-// Steps whose loads are issued together: 64 bytes a thread.
+// Steps whose loads are issued together: 128 bytes a thread, or what the registers of the
+// longer arithmetic leave room for.
+template <bool kMx, typename T>
+constexpr int kSteps = sizeof(T) == 2 ? (kMx ? 8 : 4) : 3;
 template <typename T>
-constexpr int kSteps = sizeof(T) == 2 ? 4 : 2;
+constexpr int kAmaxSteps = sizeof(T) == 2 ? 8 : 4;
+constexpr int kAmaxCtas = 4736;  // two rounds of 16 CTAs per SM
 
 template <typename Tin>
 struct Raw;
@@ -42,6 +47,12 @@ struct Raw<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void load_kept(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  // Largest magnitude as fp32 bits: bf16 bits order like the values.
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t a = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & a, v.y & a), __vmaxu2(v.z & a, v.w & a));
+    return max(m & 0xffff0000u, m << 16);
+  }
   __device__ __forceinline__ void get(float (&f)[kVec]) const {
     const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
@@ -63,6 +74,11 @@ struct Raw<float> {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ uint32_t amax() const {
+    float f[kVec];
+    get(f);
+    return amax_bits<kVec>(f);
+  }
   __device__ __forceinline__ void get(float (&f)[kVec]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -74,17 +90,27 @@ __device__ __forceinline__ uint32_t mx_codes(const float (&f)[kVec], uint32_t sb
   return sb == 255u ? 0u : e2m1x8(f, e8m0_rcp(sb));
 }
 
-// NVFP4 in fp32 with the borders settled in fp64. An fp32 quotient is off by a
-// few 2^-24; where moving it by 2^-20 either way does not change the rounded
-// result it is the correctly rounded one, and the few others are redone in fp64
-// (a block scale's 53-bit quotient or a code's cannot sit on the wrong side of a
-// border, as the borders have at most 5 bits).
+// NVFP4 in fp32, correctly rounded. An fp32 quotient is off by a few 2^-24; where moving
+// it by 2^-20 either way does not change the rounded result it is the right one. The few
+// others are redone with fp64 quotients, whose 53 bits cannot fall on the wrong side of a
+// border of at most 5. bf16 values meet borders often, as their quotients have few
+// distinct values; for them (kOften) the border b between two neighbouring results decides:
+// x / (m g) > b just as x > (b m) g, where b m is exact and the product is taken in two
+// parts. 44 x 1536 x 4096 values take 235 us with this test and 367 with fp64 quotients as
+// bf16, but 225 to 234 and 207 to 218 as fp32.
+template <bool kOften>
 struct NvScale {
   float g, r6;  // global scale, about 1 / (6 g)
   bool ok;      // g positive and finite
   __device__ __forceinline__ explicit NvScale(float gg) : g(gg) {
     ok = gg > 0.0f && gg < INFINITY;
     r6 = __fdividef(1.0f, 6.0f * gg);
+  }
+  // Sign of a - c g, a within 2^-18 of c g and both far from the ends of the range: the
+  // difference from the rounded product and the product's rounding error are both exact.
+  static __device__ __forceinline__ float side(float a, float c, float g) {
+    const float p = c * g;
+    return (a - p) - fmaf(c, g, -p);
   }
   static __device__ __noinline__ uint32_t scale_slow(float bmax, float g) {
     const double q = (double)bmax / (6.0 * (double)g);
@@ -94,6 +120,11 @@ struct NvScale {
     const double v = ldexp(rint(ldexp(q, 3 - e)), e - 3);
     return __nv_cvt_float_to_fp8((float)v, __NV_SATFINITE, __NV_E4M3);
   }
+  // The code of a block maximum b that lies between the values of codes lo and hi.
+  static __device__ __noinline__ uint32_t scale_at(float b, float g, uint32_t lo, uint32_t hi) {
+    const float over = side(b, 3.0f * (e4m3_value(lo) + e4m3_value(hi)), g);
+    return over > 0.0f || (over == 0.0f && (lo & 1u)) ? hi : lo;
+  }
   // E4M3 code of the block scale.
   __device__ __forceinline__ uint32_t scale(uint32_t m) const {
     if (!ok || m >= 0x7f800000u) return 0x7fu;
@@ -101,8 +132,24 @@ struct NvScale {
     const float q = b * r6;
     const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q * (1.0f - 0x1p-20f), q * (1.0f + 0x1p-20f)),
                                                   __NV_SATFINITE, __NV_E4M3);
-    if ((two & 0xffu) == (two >> 8) && r6 < 0x1p126f && r6 > 0x1p-120f) return two & 0xffu;
+    const bool in_range = r6 < 0x1p110f && r6 > 0x1p-110f;
+    if ((two & 0xffu) == (two >> 8) && in_range) return two & 0xffu;
+    if (kOften && in_range) return scale_at(b, g, two & 0xffu, two >> 8);
     return scale_slow(b, g);
+  }
+  // Codes lo, of that magnitude or the next where the nibbles of `open` are not zero.
+  static __device__ __noinline__ uint32_t codes_at(float4 a, float4 b, float s, float g, uint32_t lo, uint32_t open) {
+    const float f[kVec] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w = lo;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (!((open >> (4 * i)) & 7u)) continue;
+      const uint32_t c = (lo >> (4 * i)) & 7u;
+      const float border = c < 4 ? 0.25f + 0.5f * (float)c : c == 6 ? 5.0f : (float)c - 1.5f;
+      const float over = side(fabsf(f[i]), border * s, g);
+      if (over > 0.0f || (over == 0.0f && (c & 1u))) w += 1u << (4 * i);
+    }
+    return w;
   }
   static __device__ __noinline__ uint32_t code_slow(float f, double d) {
     const double a = fabs((double)f) / d;
@@ -113,9 +160,11 @@ struct NvScale {
     const float s = e4m3_value(sb);
     if (sb == 0x7fu) return 0u;
     if (s == 0.0f) return 0u;
-    const float d = s * g, r = __frcp_rn(d);
+    const float d = s * g, r = __fdividef(1.0f, d);
     const uint32_t lo = e2m1x8(f, r * (1.0f - 0x1p-20f)), hi = e2m1x8(f, r * (1.0f + 0x1p-20f));
-    if (lo == hi && d > 0x1p-120f && d < 0x1p120f) return lo;
+    if (lo == hi && d > 0x1p-110f && d < 0x1p110f) return lo;
+    if (kOften && d > 0x1p-110f && d < 0x1p110f)
+      return codes_at(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]), s, g, lo, lo ^ hi);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) w |= code_slow(f[i], (double)s * (double)g) << (4 * i);
@@ -125,7 +174,9 @@ struct NvScale {
 
 // Grid: x over a matrix's vectors, y over matrices (MXFP4 ignores matrix borders: y = 1),
 // both taken from the end: what a pass over x before this one (the global scale's) left
-// in L2 is its end, and the inverse, from the front, finds the codes written last.
+// in L2 is its end, and the inverse, from the front, finds the codes written last (24 x
+// 1001 x 1536 fp32, the three passes: 84 us instead of 86). 128 threads with 128 bytes in
+// flight each, rather than 256 with 64: bf16 to MXFP4 118 us instead of 140.
 template <bool kMx, typename Tin>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64_t vecs, const Tin* __restrict__ x,
                                                             const float* __restrict__ g, uint32_t* __restrict__ codes,
@@ -133,10 +184,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64
   pdl_wait();
   pdl_trigger();
   constexpr int kLanes = kMx ? 4 : 2;  // lanes of a block
-  constexpr int kUnroll = kSteps<Tin>;
+  constexpr int kUnroll = kSteps<kMx, Tin>;
   for (int64_t mat = n_mat - 1 - blockIdx.y; mat >= 0; mat -= gridDim.y) {
     const int64_t base = mat * vecs;
-    const NvScale nv(kMx ? 1.0f : g[mat]);
+    const NvScale<sizeof(Tin) == 2> nv(kMx ? 1.0f : g[mat]);
     const int64_t v0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
     Raw<Tin> raw[kUnroll];
 #pragma unroll
@@ -150,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(int64_t n_mat, int64
       const bool live = v < vecs;  // whole blocks: the lanes of a block agree
       float f[kVec] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (live) raw[u].get(f);
-      uint32_t m = amax_bits<kVec>(f);
+      uint32_t m = live ? raw[u].amax() : 0u;
 #pragma unroll
       for (int o = 1; o < kLanes; o *= 2) {
         const uint32_t t = __shfl_xor_sync(0xffffffffu, m, o);
@@ -172,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(int64_t n_mat, int64_t v
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t part[kThreads / 32];
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = kAmaxSteps<Tin>;
   for (int64_t mat = blockIdx.y; mat < n_mat; mat += gridDim.y) {
     uint32_t m = 0;
     for (int64_t v0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x; v0 < vecs;
@@ -184,10 +235,7 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(int64_t n_mat, int64_t v
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (v0 + u * kThreads >= vecs) break;
-        float f[kVec];
-        raw[u].get(f);
-        const uint32_t t = amax_bits<kVec>(f);
-        m = t > m ? t : m;
+        m = max(m, raw[u].amax());
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -210,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) global_scale_kernel(int64_t n_mat, f
 }
 
 // A thread writes 16 bytes a step, so that a warp's stores are whole lines: 8 bf16 values,
-// or 4 fp32 ones (half a word of codes; two 16-byte stores of a word's 8 were 10% slower).
+// or 4 fp32 ones (half a word of codes: 24 x 1001 x 1536 NVFP4 to fp32 27 us, 40 with a word's 8 by two stores).
 template <bool kMx, typename Tout>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(int64_t n_mat, int64_t vecs,
                                                               const uint32_t* __restrict__ codes,
@@ -267,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(int64_t n_mat, int
 // step; codes and scales go to every row that the token feeds, row-major
 // [rows, H/2] and [rows, H/32].
 template <int kMaxSlots>
-__global__ void __launch_bounds__(kThreads) gather_mx_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) gather_mx_kernel(const GatherParams p) {
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x;
@@ -276,12 +324,12 @@ __global__ void __launch_bounds__(kThreads) gather_mx_kernel(const GatherParams 
   for (int j = 0; j < kMaxSlots; ++j) rows[j] = j < p.S ? p.pos[t * p.S + j] : -1;
   const int nvec = p.H / kVec;  // a multiple of 32: whole warps
   const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.x) + t * p.H;
-  for (int v = threadIdx.x; v < nvec; v += kThreads) {
+  for (int v = threadIdx.x; v < nvec; v += kGatherThreads) {
     Raw<__nv_bfloat16> raw;
     raw.load(x + v * kVec);
     float f[kVec];
     raw.get(f);
-    uint32_t m = amax_bits<kVec>(f);
+    uint32_t m = raw.amax();
 #pragma unroll
     for (int o = 1; o < 4; o *= 2) {
       const uint32_t u = __shfl_xor_sync(0xffffffffu, m, o);
@@ -302,10 +350,6 @@ __global__ void __launch_bounds__(kThreads) gather_mx_kernel(const GatherParams 
 dim3 step_grid(int64_t n_mat, int64_t steps, int unroll) {
   return dim3((unsigned)ceil_div(steps, kThreads * unroll), (unsigned)(n_mat < 65535 ? n_mat : 65535));
 }
-dim3 vec_grid(int64_t n_mat, int64_t vecs, bool f32) {
-  return step_grid(n_mat, vecs, f32 ? kSteps<float> : kSteps<__nv_bfloat16>);
-}
-
 }  // namespace
 
 cudaError_t launch_quantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems, const void* x, const float* g,
@@ -315,7 +359,9 @@ cudaError_t launch_quantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems,
     n_mat = 1;
   }
   const int64_t vecs = elems / kVec;
-  const dim3 grid = vec_grid(n_mat, vecs, f32);
+  const int steps = mx ? (f32 ? kSteps<true, float> : kSteps<true, __nv_bfloat16>)
+                       : (f32 ? kSteps<false, float> : kSteps<false, __nv_bfloat16>);
+  const dim3 grid = step_grid(n_mat, vecs, steps);
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   const float* xf = static_cast<const float*>(x);
@@ -332,8 +378,9 @@ cudaError_t launch_fp4_global_scale(bool f32, int64_t n_mat, int64_t elems, cons
   cudaError_t e = cudaMemsetAsync(g, 0, (size_t)n_mat * 4, s);
   if (e != cudaSuccess) return e;
   const int64_t vecs = elems / kVec;
-  dim3 grid = vec_grid(n_mat, vecs, f32);
-  if (grid.x > 1024) grid.x = 1024;
+  dim3 grid = step_grid(n_mat, vecs, f32 ? kAmaxSteps<float> : kAmaxSteps<__nv_bfloat16>);
+  const unsigned most = (unsigned)ceil_div(kAmaxCtas, grid.y);
+  if (grid.x > most) grid.x = most;
   uint32_t* gb = reinterpret_cast<uint32_t*>(g);
   e = f32 ? launch_pdl(amax_kernel<float>, grid, dim3(kThreads), 0, s, 1, n_mat, vecs, static_cast<const float*>(x), gb)
           : launch_pdl(amax_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, 1, n_mat, vecs,
@@ -364,7 +411,7 @@ cudaError_t launch_dequantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elem
 
 cudaError_t launch_gather_mx(const GatherParams& p, cudaStream_t s) {
   if (p.T == 0) return cudaSuccess;
-  const dim3 grid((unsigned)p.T), block(kThreads);
+  const dim3 grid((unsigned)p.T), block(kGatherThreads);
   if (p.S <= 9) return launch_pdl(gather_mx_kernel<9>, grid, block, 0, s, 1, p);
   return launch_pdl(gather_mx_kernel<kMaxTopK + 1>, grid, block, 0, s, 1, p);
 }

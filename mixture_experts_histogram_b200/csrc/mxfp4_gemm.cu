@@ -32,7 +32,7 @@
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 scale writers, 6..13 epilogue.
 //
 // Measured (H = 4096, I = 1536): 16 tokens on 88 experts, single CTAs: gate/up 82 us, 468
-// MB at 68% of DRAM peak, the weight stream. 8192 tokens on 352 experts, pairs: gate/up 625
+// MB at 69% of DRAM peak, the weight stream. 8192 tokens on 352 experts, pairs: gate/up 625
 // us (3.0 PFLOP/s) and down 390 us (2.4); loads alone, without MMAs and epilogue, take 462
 // and 358 us, so the tiles' way from L2 bounds the second and most of the first (the
 // layer on single CTAs: 1.35 ms, on pairs 1.20).

@@ -99,6 +99,32 @@ def test_nvfp4_quantize_exact(m, n, rows, k, kind):
         assert np.array_equal(y.cpu().numpy(), ref.nv_values(c, s, gs).astype(np.float32))  # one rounding
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_nvfp4_borders_of_every_amax(m, kind):
+    """Every bf16 mantissa as a matrix's largest value and many others below it: quotients on, and a
+    rounding of the global scale away from, the borders between codes and between scales; then global
+    scales near the ends of the range."""
+    import torch
+    rng = np.random.default_rng(91)
+    n, rows, k = 128, 6, 256
+    x = rng.integers(128, 256, (n, rows, k)).astype(np.float32) * np.exp2(rng.integers(-9, 0, (n, rows, 1))).astype(np.float32)
+    x *= np.exp2(rng.integers(-4, 1, (n, rows, k))).astype(np.float32) * rng.choice([-1.0, 1.0], (n, rows, k)).astype(np.float32)
+    x[:, 0, 0] = np.arange(128, 256)  # the others are below 128
+    xt = _tensor(x, kind)
+    g = torch.empty(n, dtype=torch.float32, device="cuda")
+    m.moe_fp4_global_scale(n, rows, k, xt, g)
+    own = (np.abs(x).max((1, 2)) / np.float32(2688)).astype(np.float32)
+    assert np.array_equal(g.cpu().numpy(), own)
+    codes = torch.empty((n, rows, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n, rows, k // 16), dtype=torch.uint8, device="cuda")
+    for gs, f in ((own, 1.0), (own * np.float32(2.0 ** 105), 2.0 ** 105), (own * np.float32(2.0 ** -115), 2.0 ** -115)):
+        xs = x * np.float32(f)
+        m.moe_quantize_fp4(m.MOE_WDTYPE_NVFP4, n, rows, k, _tensor(xs, kind), m.to_device(gs), codes, scales)
+        c, sc = ref.nv_quantize(xs, gs)
+        assert np.array_equal(scales.cpu().numpy(), sc)
+        assert np.array_equal(codes.cpu().numpy(), c)
+
+
 def test_quantize_non_finite_and_bf16_output(m):
     """A block with an infinity or NaN gets the NaN scale and zero codes; its neighbours do not change."""
     import torch
