@@ -1138,16 +1138,25 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
       return o;
     };
     int freed = 0, told = 0;  // entries whose rows are free again, and that this warp has reported
+    auto until_freed = [&](int i) {  // entry i's rows are free again
+      for (; ok && freed <= i; ++freed)
+        ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c, i,
+                              p.wait_ns);
+    };
     bool dry = true;
     Step st{0, 0, 0, 0, 1u};
     Values cur = fetch(st);
 #pragma unroll 1
     while (true) {
       if (!dry) {
-        // Every entry before this step's has this warp's rows.
+        // Every entry before this step's has this warp's rows. An entry is reported once the
+        // one a ring before it has been used: hfull counts arrivals whoever they come from,
+        // and an earlier one would stand for a warp that has yet to report that older entry.
         __syncwarp();
-        for (; told < min(st.i, U); ++told)
+        for (; told < min(st.i, U); ++told) {
+          until_freed(told - kHRing);
           if (lane == 0) mbar_arrive(&hfull[told % kHRing]);
+        }
         if (st.i >= U) break;
       }
       const Step nx = dry ? st : after(st);
@@ -1155,11 +1164,7 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
       if (!dry && st.j == 0) {
         // Room for the row: first[] counts on from entry to entry, the oldest go first.
         const int end = first[st.i] + st.r + 1;
-        while (ok && (freed <= st.i - kHRing || first[freed] < end - h_rows)) {
-          ok = warp_wait<false>(&hempty[freed % kHRing], (uint32_t)(freed / kHRing) & 1u, p.status, abort_flag, 0x200c,
-                                st.i, p.wait_ns);
-          ++freed;
-        }
+        while (ok && first[freed] < end - h_rows) until_freed(freed);
       }
       uint8_t* row = act + (dry ? 0 : by_rows.rem(first[st.i] + st.r)) * hpitch;
 #pragma unroll

@@ -241,3 +241,66 @@ def test_few_wait_runs_out(m):
         m.moe_debug_inject(m.MOE_INJECT_NONE, 0)
     assert np.array_equal(bits(call(x)), first)
     assert m.moe_read_status(call.ws) == 0
+
+
+def device_weights(w, seed, E, S, H, I):
+    """Random weights of one storage made on the device (variance about 1 / inputs), for tests that
+    compare calls with calls."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, shape[-1] ** -0.5, generator=gen)
+
+    def bytes_of(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, dtype=torch.uint8, device="cuda", generator=gen)
+
+    wt = {"router_w": normal(E, H), "router_bias": None}
+    for pre, n in (("", E), ("s", 1))[: 1 + S]:
+        for name, rows, cols in (("1", I, H), ("3", I, H), ("2", H, I)):
+            code, scale, glob = pre + "w" + name, pre + "s" + name, pre + "g" + name
+            if w == 0:
+                wt[code] = normal(n, rows, cols)
+            elif w == 1:
+                wt[code] = (normal(n, rows, cols) * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+                wt[scale] = torch.full((n, rows // 128, cols // 128), 1 / 64, device="cuda")
+            else:  # uniform codes, root mean square 2.93
+                wt[code] = bytes_of(0, 256, n, rows, cols // 2)
+                if w == 2:
+                    wt[scale] = bytes_of(0x30, 0x40, n, rows, cols // 16)  # 0.5 .. 1.9
+                    wt[glob] = torch.full((n,), cols ** -0.5 / 3, device="cuda")
+                else:
+                    mid = 127 + round(np.log2(cols ** -0.5 / 2.93))
+                    wt[scale] = bytes_of(mid - 1, mid + 2, n, rows, cols // 32)
+    return wt
+
+
+def device_call(m, w, T, H, I, E, k, S, wt):
+    """A Call on weights that are on the device already."""
+    call = Call(m, w, T, H, I, E, k, S, {})
+    call.dev, call.w = wt, m.make_weights(wt)
+    return call
+
+
+# T, H, I, E, k: the space of x holds 25 to 60 rows of h, and more than 24 experts are chosen
+RINGS = [(8, 4096, 512, 200, 8), (5, 4096, 512, 200, 8), (8, 7168, 2048, 48, 8), (8, 4096, 1024, 88, 8)]
+
+
+@pytest.mark.parametrize("w", [0, 1, 2, 3], ids=lambda w: FMT[w])
+@pytest.mark.parametrize("T,H,I,E,k", RINGS)
+def test_few_many_rows_of_h(m, w, T, H, I, E, k):
+    """Rows of h for more experts than the ring has slots, with room for 25 rows or more (so that the
+    slots and not the rows run out): every call gives the bits of one-token calls."""
+    import torch
+    wt = device_weights(w, 90, E, 1, H, I)
+    x = m.to_device(synth.normal_bf16(91, 1, (T, H), 1.0))
+    one, call = (device_call(m, w, n, H, I, E, k, 1, wt) for n in (1, T))
+    want = torch.cat([one(x[t:t + 1]).clone() for t in range(T)])
+    assert torch.isfinite(want.float()).all()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        call.out.fill_(0)
+        differ += (call(x).view(torch.int16) != want.view(torch.int16)).sum()
+    assert len(set(call.idx.flatten().tolist())) + 1 > 25
+    assert differ.item() == 0
+    assert m.moe_read_status(call.ws) == 0
