@@ -662,6 +662,42 @@ int run_combine(const moe_config* c, int64_t T, const void* y, const int32_t* po
   return MOE_OK;
 }
 
+// Consecutive 1 KiB-aligned regions of a workspace.
+struct Regions {
+  size_t end = 0;
+  size_t operator()(size_t bytes) {
+    const size_t o = end;
+    end = (size_t)round_up((int64_t)(end + (bytes ? bytes : 1)), 1024);
+    return o;
+  }
+};
+
+// The workspace of the few-token layer, 1 <= T <= MOE_FEW_MAX_TOKENS: a layout of its
+// own over the same memory (fp32 h for 8 tokens of every list entry outweighs all that the
+// other entry points need of so few tokens). The status word comes first in both.
+struct FewLayout {
+  size_t status, logits, counter, x, h, total;
+};
+
+FewLayout few_layout(const moe_config& c, int T) {
+  FewLayout F;
+  Regions take;
+  F.status = take(kStatusBytes);
+  F.logits = take((size_t)T * c.n_experts * 4);
+  F.counter = take(4);
+  F.x = take((size_t)few_x_bytes(c.wdtype, T, c.hidden));
+  F.h = take((size_t)(T * c.top_k + c.n_shared) * MOE_FEW_MAX_TOKENS * c.inter * 4);
+  F.total = take.end;
+  return F;
+}
+
+// The most workspace that the few-token layer takes for up to T tokens of this layer.
+size_t few_workspace(const moe_config& c, int64_t T) {
+  for (int t = (int)(T < MOE_FEW_MAX_TOKENS ? T : MOE_FEW_MAX_TOKENS); t > 0; --t)
+    if (few_fits(c.wdtype, t, c.hidden, c.inter, kRouterTargetCtas)) return few_layout(c, t).total;
+  return 0;
+}
+
 int check_ws(const moe_config* c, int64_t T, void* ws, size_t ws_bytes, WsLayout* L) {
   if (!ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
@@ -694,12 +730,7 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   int64_t ks = target_ctas / m_tiles;
   const int64_t kmax = c.hidden / 64 < 16 ? c.hidden / 64 : 16;
   L.ksplit = ks < 1 ? 1 : (ks > kmax ? kmax : ks);
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off = (size_t)round_up((int64_t)(off + (bytes ? bytes : 1)), 1024);
-    return o;
-  };
+  Regions take;
   L.status = take(kStatusBytes);  // status word, first-timeout record, debug counters
   L.idx = take((size_t)T * k * 4);
   L.gate = take((size_t)T * k * 4);
@@ -722,13 +753,7 @@ WsLayout ws_layout(const moe_config& c, int64_t T, int target_ctas) {
   L.part = take(k2 > 1 ? (size_t)k2 * L.R * c.hidden * 4 : 0);
   L.x_stage = take((size_t)T * c.hidden * 2);
   L.out_stage = take((size_t)T * c.hidden * 2);
-  if (T > 0 && T <= MOE_FEW_MAX_TOKENS) {
-    // The few-token layer: list entries x 8 token slots of h.
-    L.few_counter = take(4);
-    L.few_x = take((size_t)few_x_bytes(c.wdtype, (int)T, c.hidden));
-    L.few_h = take((size_t)(T * k + S) * MOE_FEW_MAX_TOKENS * c.inter * 4);
-  }
-  L.total = off;
+  L.total = take.end;
   return L;
 }
 
@@ -742,7 +767,8 @@ int moe_workspace_bytes(const moe_config* cfg, int64_t T, size_t* bytes) {
   const int rc = check_config(cfg, T);
   if (rc != MOE_OK) return rc;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = ws_layout(*cfg, T, kRouterTargetCtas).total;
+  const size_t most = ws_layout(*cfg, T, kRouterTargetCtas).total, few = few_workspace(*cfg, T);
+  *bytes = most > few ? most : few;
   return MOE_OK;
 }
 
@@ -780,8 +806,10 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   if (!aligned(x, 16) || !aligned(out, 16)) return MOE_ERR_MISALIGNED;
   if ((topk_idx == nullptr) != (topk_w == nullptr)) return MOE_ERR_INVALID_ARG;
   if (T && !few_fits(cfg->wdtype, (int)T, cfg->hidden, cfg->inter, kRouterTargetCtas)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  WsLayout L;
-  if ((rc = check_ws(cfg, T, workspace, workspace_bytes, &L)) != MOE_OK) return rc;
+  if (!workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+  const FewLayout L = few_layout(*cfg, (int)T);
+  if (T && workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (T == 0) return MOE_OK;
   const int sms = sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -801,10 +829,10 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.out = static_cast<__nv_bfloat16*>(out);
   p.topk_idx = topk_idx;
   p.topk_w = topk_w;
-  p.logits = reinterpret_cast<float*>(ws + L.logits_part);
-  p.xrows = ws + L.few_x;
-  p.h = reinterpret_cast<float*>(ws + L.few_h);
-  p.counter = reinterpret_cast<int*>(ws + L.few_counter);
+  p.logits = reinterpret_cast<float*>(ws + L.logits);
+  p.xrows = ws + L.x;
+  p.h = reinterpret_cast<float*>(ws + L.h);
+  p.counter = reinterpret_cast<int*>(ws + L.counter);
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.wait_ns = g_wait_ns;
   p.inject = g_inject;

@@ -28,9 +28,7 @@ __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_
 struct WsLayout {
   int64_t T, R, rows_pad, chunks, ksplit;
   size_t status, idx, gate, logits_part, chunk_base, counts, offsets, mt_prefix, mp_prefix;
-  size_t perm, pos, row_gate, xp, sxp, h, sh, y, part, x_stage, out_stage;
-  size_t few_counter, few_x, few_h;  // T <= MOE_FEW_MAX_TOKENS only
-  size_t total;
+  size_t perm, pos, row_gate, xp, sxp, h, sh, y, part, x_stage, out_stage, total;
 };
 
 WsLayout ws_layout(const moe_config& c, int64_t T, int num_sms);

@@ -304,3 +304,25 @@ def test_few_many_rows_of_h(m, w, T, H, I, E, k):
     assert len(set(call.idx.flatten().tolist())) + 1 > 25
     assert differ.item() == 0
     assert m.moe_read_status(call.ws) == 0
+
+
+@pytest.mark.parametrize("w", [0, 1, 2, 3], ids=lambda w: FMT[w])
+def test_few_workspace_of_a_larger_batch(m, w):
+    """A 16-token workspace serves the whole layer and the few-token one for 8 tokens; neither
+    writes behind the size asked for its own tokens."""
+    import torch
+    T, H, I, E, k = 8, 1024, 512, 40, 4
+    wt = device_weights(w, 92, E, 1, H, I)
+    x = m.to_device(synth.normal_bf16(93, 1, (T, H), 1.0))
+    call = device_call(m, w, T, H, I, E, k, 1, wt)
+    few = call(x).clone()
+    whole = torch.empty_like(few)
+    m.moe_forward(call.cfg, T, x, call.w, whole, call.ws)
+    for nb in (m.moe_workspace_bytes(call.cfg, T), m.moe_workspace_bytes(call.cfg, 16)):
+        mem = torch.full((nb + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        call.ws = mem[:nb]
+        assert torch.equal(call(x).view(torch.int16), few.view(torch.int16))
+        again = torch.empty_like(whole)
+        m.moe_forward(call.cfg, T, x, call.w, again, call.ws)
+        assert torch.equal(again.view(torch.int16), whole.view(torch.int16))
+        assert (mem[nb:] == 0xA5).all()
