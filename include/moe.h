@@ -133,10 +133,9 @@ typedef struct moe_weights {
   const float* sg2;
 } moe_weights;
 
-/* Bytes of workspace that every entry point needs for T tokens; moe_forward_few
- * needs more for up to 8 than the others, which is counted for every T >= 1, so a
- * workspace for T tokens serves calls of up to 8 tokens as well. Host only; touches
- * no device. */
+/* Bytes of workspace that every entry point needs for any number of tokens up to T:
+ * the size never falls as T grows (what moe_forward_few needs for up to 8 tokens is
+ * counted for every T >= 1). Host only; touches no device. */
 MOE_API int moe_workspace_bytes(const moe_config* cfg, int64_t T, size_t* bytes);
 
 /*

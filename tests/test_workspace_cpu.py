@@ -63,3 +63,26 @@ def test_few_token_scratch_is_asked_for_by_its_call_only(lib, w, before):
     cfg = m.make_config(4096, 352, 8, 1, 1536, w)
     for name, rc in calls(lib, cfg, 8, before):
         assert rc == (m.MOE_ERR_WORKSPACE_TOO_SMALL if name == "moe_forward_few" else m.MOE_ERR_CUDA), (name, rc)
+
+
+@pytest.mark.parametrize("w", range(4))
+@pytest.mark.parametrize("layer", LAYERS + [(4096, 1, 1, 0, 11264), (128, 1, 1, 0, 128), (2048, 512, 16, 1, 512)])
+def test_size_never_falls_where_splits_end(lib, w, layer):
+    """Counts around those at which the router's logits or the down GEMM's sums are split less, and a few
+    far ones."""
+    if w >= 2 and (layer[0] % 512 or layer[4] % 512):
+        pytest.skip("not a shape of this storage")
+    cfg = m.make_config(*layer[:4], layer[4], w)
+    tokens = sorted({t for n in range(1, 160) for t in (128 * n, 128 * n + 1)} | set(range(1, 300)) | {1 << 18, 1 << 20})
+    sizes = [m.moe_workspace_bytes(cfg, T) for T in tokens]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.skipif(cuda_available(), reason="calls with buffers that do not exist end at the missing device")
+def test_one_workspace_where_splits_end(lib):
+    """1152 tokens take more partial logits than 1153; the larger batch's workspace serves them."""
+    cfg = m.make_config(512, 512, 1, 0, 512, 3)
+    nb = m.moe_workspace_bytes(cfg, 1153)
+    for T in (1, 8, 9, 1151, 1152, 1153):
+        for name, rc in calls(lib, cfg, T, nb):
+            assert rc == m.MOE_ERR_CUDA, (name, T, rc)
