@@ -861,6 +861,9 @@ int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_w
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.wait_ns = g_wait_ns;
   p.inject = g_inject;
+  // (Before the tensor maps: a host thread's first call has no context yet, and this is what
+  // gives it one.)
+  CUDA_TRY(prepare_few(cfg->wdtype));
   if (!get_encoder()) return MOE_ERR_CUDA;
   FewMaps tm{};
   const int per2 = cfg->wdtype == MOE_WDTYPE_BF16 ? 1 : cfg->wdtype == MOE_WDTYPE_FP8_E4M3 ? 2 : 4;

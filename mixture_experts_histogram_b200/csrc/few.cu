@@ -1327,18 +1327,22 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
 }
 
 template <int kW>
+cudaError_t prepare_one() {
+  // The router CTAs ask for the shared-memory split of the second kernel, whose CTAs
+  // could otherwise not start on their SMs before they end.
+  return cudaFuncSetAttribute(few_router_kernel<kW>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
+
+template <int kW>
 cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) {
   auto kern = few_experts_kernel<kW>;
   p.n_stages = Smem<kW>::stages(p.T, p.H, p.I);
   const int smem = Smem<kW>::tile_offset(p.T, p.H, p.I, p.n_stages) + p.n_stages * kRows * Fmt<kW>::kSlab + 1024;
+  auto router = few_router_kernel<kW>;
+  const unsigned ctas = (unsigned)(ceil_div(p.E, kRouterExperts) + ceil_div((int64_t)p.T * p.H / 8, kRouterThreads));
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // The router CTAs ask for the shared-memory split of the second kernel, whose CTAs
-  // could otherwise not start on their SMs before they end.
-  auto router = few_router_kernel<kW>;
-  e = cudaFuncSetAttribute(router, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  const unsigned ctas = (unsigned)(ceil_div(p.E, kRouterExperts) + ceil_div((int64_t)p.T * p.H / 8, kRouterThreads));
   e = launch_pdl(router, dim3(ctas), dim3(kRouterThreads), 0, s, 1, p);
   if (e != cudaSuccess) return e;
   // Cooperative: the CTAs wait for one another, so all of them have to be resident.
@@ -1381,6 +1385,15 @@ bool few_fits(int wdtype, int T, int H, int I, int sms) {
     case MOE_WDTYPE_FP8_E4M3: return fits<MOE_WDTYPE_FP8_E4M3>(T, H, I, sms);
     case MOE_WDTYPE_NVFP4: return fits<MOE_WDTYPE_NVFP4>(T, H, I, sms);
     default: return fits<MOE_WDTYPE_MXFP4>(T, H, I, sms);
+  }
+}
+
+cudaError_t prepare_few(int wdtype) {
+  switch (wdtype) {
+    case MOE_WDTYPE_BF16: return prepare_one<MOE_WDTYPE_BF16>();
+    case MOE_WDTYPE_FP8_E4M3: return prepare_one<MOE_WDTYPE_FP8_E4M3>();
+    case MOE_WDTYPE_NVFP4: return prepare_one<MOE_WDTYPE_NVFP4>();
+    default: return prepare_one<MOE_WDTYPE_MXFP4>();
   }
 }
 

@@ -58,6 +58,7 @@ struct FewMaps {
 // Whether T tokens leave room for the weight ring in shared memory.
 bool few_fits(int wdtype, int T, int H, int I, int sms);
 int64_t few_x_bytes(int wdtype, int T, int H);  // of FewParams::xrows
+cudaError_t prepare_few(int wdtype);  // the kernels' settings, before each launch_few
 cudaError_t launch_few(const FewParams& p, const FewMaps& tm, int wdtype, int sms, cudaStream_t s);
 
 }  // namespace moe
