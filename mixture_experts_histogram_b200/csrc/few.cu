@@ -1328,6 +1328,11 @@ __global__ void __launch_bounds__(Smem<kW>::kThreads, 1)
 
 template <int kW>
 cudaError_t prepare_one() {
+  // The limit belongs to the function: the same for every call, or another host thread's
+  // smaller one could come between this and the launch.
+  const cudaError_t e =
+      cudaFuncSetAttribute(few_experts_kernel<kW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e != cudaSuccess) return e;
   // The router CTAs ask for the shared-memory split of the second kernel, whose CTAs
   // could otherwise not start on their SMs before they end.
   return cudaFuncSetAttribute(few_router_kernel<kW>, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -1341,9 +1346,7 @@ cudaError_t launch_one(FewParams p, const FewMaps& tm, int sms, cudaStream_t s) 
   const int smem = Smem<kW>::tile_offset(p.T, p.H, p.I, p.n_stages) + p.n_stages * kRows * Fmt<kW>::kSlab + 1024;
   auto router = few_router_kernel<kW>;
   const unsigned ctas = (unsigned)(ceil_div(p.E, kRouterExperts) + ceil_div((int64_t)p.T * p.H / 8, kRouterThreads));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(router, dim3(ctas), dim3(kRouterThreads), 0, s, 1, p);
+  const cudaError_t e = launch_pdl(router, dim3(ctas), dim3(kRouterThreads), 0, s, 1, p);
   if (e != cudaSuccess) return e;
   // Cooperative: the CTAs wait for one another, so all of them have to be resident.
   cudaLaunchConfig_t cfg = {};

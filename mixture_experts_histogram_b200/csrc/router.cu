@@ -27,12 +27,14 @@ namespace {
 constexpr int kRouterThreads = 192;
 constexpr int kRouterMaxStages = 4;
 constexpr int kASmem = kTileM * kStageBytesK;  // 16 KB of x per stage
+constexpr int kRouterRing = 200 * 1024;        // the stages take no more than this
+constexpr int kRouterMaxSmem = 1024 + kRouterRing + 256;
 
 __host__ __device__ inline int router_b_bytes(const RouterParams& p) { return p.nbox * p.box_rows * kStageBytesK; }
 
 __host__ __device__ inline int router_stages(const RouterParams& p) {
   const int per = kASmem + router_b_bytes(p);
-  int st = (200 * 1024) / per;
+  int st = kRouterRing / per;
   return st > kRouterMaxStages ? kRouterMaxStages : st;
 }
 
@@ -315,7 +317,8 @@ cudaError_t launch_router_gemm(const RouterParams& p, const CUtensorMap& tm_x, c
                                cudaStream_t s) {
   const int stages = router_stages(p);
   const size_t smem = 1024 + (size_t)stages * (kASmem + router_b_bytes(p)) + 256;
-  cudaError_t e = cudaFuncSetAttribute(router_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the same for every call: it belongs to the function, whoever launches it.
+  cudaError_t e = cudaFuncSetAttribute(router_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouterMaxSmem);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)ceil_div(p.T, kTileM), (unsigned)p.ksplit);
   return launch_pdl(router_gemm_kernel, grid, dim3(kRouterThreads), smem, s, 1, p, tm_x, tm_w);
