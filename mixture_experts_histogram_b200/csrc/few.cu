@@ -380,8 +380,8 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
 
 // 8 values of a row (inputs 8 v .. 8 v + 7; all lanes of the warp take part, `live`
 // ones hold values) into the operand row at `row` with scales behind it. FP8:
-// kDivide quantises by IEEE quotients (x, as moe_quantize_act defines it), else by
-// products with approximate reciprocals (h, whose own fp32 noise is larger).
+// kDivide quantises by quotients (x, as moe_quantize_act defines it), else by products
+// with the scale's reciprocal, correctly rounded (h, as the grouped GEMMs do).
 template <int kW, bool kDivide>
 __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v, const float (&f)[8], bool live) {
   using F = Fmt<kW>;
@@ -406,8 +406,8 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
       // (A NaN fails the comparison, keeps scale 1 and becomes a NaN code.)
       const float amax = __uint_as_float(m);
-      s = amax > 0.0f ? (kDivide ? __fdiv_rn(amax, 448.0f) : amax * (1.0f / 448.0f)) : 1.0f;
-      const float r = kDivide ? 1.0f : __fdividef(1.0f, s);
+      s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      const float r = kDivide ? 1.0f : __frcp_rn(s);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 q = kDivide ? make_float2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s))
