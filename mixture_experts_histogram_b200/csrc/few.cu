@@ -406,12 +406,13 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
       // (A NaN fails the comparison, keeps scale 1 and becomes a NaN code.)
       const float amax = __uint_as_float(m);
-      s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-      const float r = kDivide ? 1.0f : __frcp_rn(s);
+      s = e4m3_scale(amax);
+      const float up = !kDivide && e4m3_tiny(s) ? kE4m3Lift : 1.0f;
+      const float r = kDivide ? 1.0f : __frcp_rn(s * up);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 q = kDivide ? make_float2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s))
-                                 : make_float2(f[2 * j] * r, f[2 * j + 1] * r);
+                                 : make_float2(f[2 * j] * up * r, f[2 * j + 1] * up * r);
         h[j] = f16x2_of_e4m3x2(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
       }
     } else if constexpr (kW == MOE_WDTYPE_MXFP4) {

@@ -42,6 +42,17 @@ __device__ __forceinline__ Item decode_item(int item, int n_tiles, int G, int ti
 // largest per-token error of the layer, so it is not used.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// E4M3 block scale of h, blockmax / 448, at least the smallest fp32 number; 1 for zeros.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  return amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-149f) : 1.0f;
+}
+
+// A subnormal scale's reciprocal would overflow from 2^-128 down (values of 1e-36 and
+// less; a zero times infinity is NaN): there values and scale are first multiplied by
+// kE4m3Lift, which is exact.
+constexpr float kE4m3Lift = 0x1p64f;
+__device__ __forceinline__ bool e4m3_tiny(float s) { return s < 0x1p-126f; }
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);

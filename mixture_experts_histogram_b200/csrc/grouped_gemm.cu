@@ -590,8 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ax[hf * 128 + rl] = amax;
           named_bar_sync(1 + q, 64);
           amax = fmaxf(amax, ax[(1 - hf) * 128 + rl]);
-          const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          const float inv = amax > 0.0f ? __frcp_rn(s) : 0.0f;
+          const float s = e4m3_scale(amax);
+          float inv = amax > 0.0f ? __frcp_rn(s) : 0.0f;
+          if (e4m3_tiny(s)) {
+            inv = __frcp_rn(s * kE4m3Lift);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              acc[i].x *= kE4m3Lift;
+              acc[i].y *= kE4m3Lift;
+            }
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {

@@ -380,11 +380,11 @@ __global__ void __launch_bounds__(kSwThreads, 1)
         for (int i = 0; i < 16; ++i) {
           const float* a4 = amax_s + hf * 64 + i;
           const float amax = fmaxf(fmaxf(a4[0], a4[16]), fmaxf(a4[32], a4[48]));
-          const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-          const float inv = amax > 0.0f ? __frcp_rn(s) : 0.0f;
+          const float s = e4m3_scale(amax), up = e4m3_tiny(s) ? kE4m3Lift : 1.0f;
+          const float inv = amax > 0.0f ? __frcp_rn(s * up) : 0.0f;
           const int64_t row = (int64_t)it.row0 + 16 * hf + i;
           if (ok && row < it.end) {
-            const __nv_fp8_storage_t code = __nv_cvt_float_to_fp8(h[i] * inv, __NV_SATFINITE, __NV_E4M3);
+            const __nv_fp8_storage_t code = __nv_cvt_float_to_fp8(h[i] * up * inv, __NV_SATFINITE, __NV_E4M3);
             static_cast<uint8_t*>(p.out)[row * p.N + jcol] = (uint8_t)code;
             if (q == 0 && lane == 0) p.out_scale[(int64_t)it.n * p.rows_pad + row] = s;
           }

@@ -10,7 +10,7 @@ import pytest
 import fp4_ref as ref
 import synth
 from conftest import cuda_available
-from parity import bf16_bits_to_f64
+from parity import bf16_bits_to_f64, rows_rel
 from test_gpu_few import Call, bits, m  # noqa: F401 (m: fixture)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="needs a CUDA device")]
@@ -76,3 +76,38 @@ def test_few_rounds_h_as_the_layer(m, variant):  # noqa: F811
         v = bf16_bits_to_f64(few)
         # codes 448 and 16 to 32 of one scale: 14 at least, less the two bf16 roundings
         assert (v[:, ::128] > 13.8 * v[:, 1::128]).all() and (v > 0).all()
+
+
+@pytest.mark.parametrize("size", [1e-19, 3e-21, 3e-23])
+def test_tiny_tokens_stay_finite(m, variant, size):  # noqa: F811
+    """Tokens whose h blocks have subnormal scales (h goes as x squared), some of h exactly zero: the
+    definition's outputs, not the NaN of an infinite reciprocal. At the last size h is a few of the
+    smallest fp32 numbers, and the outputs have to be finite."""
+    rng = np.random.default_rng(5)
+    n, k, S = 4, 2, 1
+    wt = {"router_w": synth.f32_to_bf16(np.zeros((n, H), np.float32)),
+          "router_bias": np.arange(n, dtype=np.float32)}
+    for pre, c in (("", n), ("s", S)):
+        for name in "132":
+            code = rng.integers(0, 256, (c, H, I)).astype(np.uint8)
+            code[(code & 127) > 0x60] &= 0x9F
+            if name == "3":
+                code[:, ::5] = 0  # no up sum: h is zero
+            wt[pre + "w" + name] = code
+            wt[pre + "s" + name] = np.full((c, 2, 2), 2.0 ** 40 if name == "2" else 2.0 ** -6, np.float32)
+    xh = synth.f32_to_bf16((rng.standard_normal((T, H)) * size).astype(np.float32))
+    call = Call(m, 1, T, H, I, n, k, S, wt)
+    x = m.to_device(xh)
+    outs = [bf16_bits_to_f64(bits(o)) for o in (call(x), forward(m, call, x))]
+    assert m.moe_read_status(call.ws) == 0
+    e = np.exp([1.0, 0.0])
+    idx, gate = np.tile([n - 1, n - 2], (T, 1)), np.tile(e / e.sum(), (T, 1))
+
+    def of(pre):
+        return lambda j=0: [ref.e4m3_table()[wt[pre + "w" + i][j]] * np.kron(wt[pre + "s" + i][j], np.ones((128, 128)))
+                            for i in "132"]
+    for out in outs:
+        assert np.isfinite(out).all()
+    if size > 1e-21:
+        want = ref.layer("fp8", synth.bf16_to_f32(xh).astype(np.float64), idx, gate, of(""), of("s"))
+        assert max(rows_rel(out, want).max() for out in outs) < 2e-2
