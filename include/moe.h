@@ -159,8 +159,9 @@ MOE_API int moe_forward(const moe_config* cfg, int64_t T, const void* x, const m
  * are gate-weighted and summed in fp32 without an intermediate rounding, by
  * ascending index and the shared expert last: a token's result does not depend on
  * the other tokens of the call. The tokens' activations must leave room for the
- * weight ring in shared memory (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * max(H, I)
- * <= 65,536 always does. The cooperative launch starts when every SM is free: it
+ * weight ring in shared memory, and a CTA's share of the outputs for their sums
+ * (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * max(H, I) <= 65,536 with H <= 256 x the
+ * number of SMs (37,888 on 148) always does. The cooperative launch starts when every SM is free: it
  * waits for kernels of other streams to end. One workspace serves one call at a time.
  */
 enum { MOE_FEW_MAX_TOKENS = 8 };

@@ -145,3 +145,22 @@ def test_few_workspace(lib):
     sizes = [m.moe_workspace_bytes(cfg, T) for T in range(1, 10)]
     assert all(a < b for a, b in zip(sizes[:8], sizes[1:8]))
     assert sizes[7] > 65 * 8 * 1536 * 4  # h of (8 x 8 + 1) experts in fp32
+
+
+def test_few_sizes_that_always_fit(lib):
+    """What moe.h promises: T * max(H, I) <= 65,536 with H <= 256 x 148 is accepted; a larger H is not."""
+    fake = m.moe_weights(*[1 << 20 for _ in m.WEIGHT_FIELDS])
+
+    def call(w, T, H, I):
+        cfg = m.make_config(H, 16, 2, 1, I, w)
+        return lib.moe_forward_few(ctypes.byref(cfg), T, 1024, ctypes.byref(fake), 2048, None, None, 4096, 16, None)
+    for w in range(4):
+        unit = (128, 128, 256, 512)[w]
+        for T in range(1, m.MOE_FEW_MAX_TOKENS + 1):
+            most = 65536 // T // unit * unit
+            top = min(most, 37888 // unit * unit)
+            for H in {unit, top // 2 // unit * unit, top - unit, top}:
+                for I in {unit, most // 2 // unit * unit, most}:
+                    assert call(w, T, H, I) == m.MOE_ERR_WORKSPACE_TOO_SMALL, (w, T, H, I)  # all else in order
+        for H in (37888 // unit * unit + unit, 40960, 65536):
+            assert call(w, 1, H, unit) == m.MOE_ERR_UNSUPPORTED_SHAPE, (w, H)
