@@ -249,12 +249,16 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(int64_t n_mat, int64_t v
   }
 }
 
-// g = amax / (6 * 448), rounded once; 1 for an all-zero matrix.
+// g = amax / (6 * 448), rounded once; 1 for an all-zero matrix. A quotient that rounds to
+// zero (amax below 2^-138.6) becomes the smallest fp32 number: with g = 0 a finite matrix
+// would have no codes.
 __global__ void __launch_bounds__(kThreads) global_scale_kernel(int64_t n_mat, float* g) {
   pdl_wait();
   pdl_trigger();
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < n_mat) g[i] = g[i] == 0.0f ? 1.0f : __fdiv_rn(g[i], 2688.0f);
+  if (i >= n_mat) return;
+  const float q = __fdiv_rn(g[i], 2688.0f);
+  g[i] = g[i] == 0.0f ? 1.0f : q == 0.0f ? 0x1p-149f : q;
 }
 
 // A thread writes 16 bytes a step, so that a warp's stores are whole lines: 8 bf16 values,

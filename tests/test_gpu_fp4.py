@@ -431,3 +431,30 @@ def test_quantize_beyond_32_bits(m):
         y = torch.empty_like(x)
         m.moe_dequantize_fp4(fmt, n, rows, k, codes, scales, g, y)
         assert torch.equal(y, x)
+
+
+def test_nvfp4_tiniest_matrices(m):
+    """Largest values from the smallest fp32 number up, where amax / 2688 rounds to zero or to few bits:
+    the matrices read back as the definition says, not as NaN."""
+    import torch
+    rng = np.random.default_rng(92)
+    top = np.array([1, 2, 3, 700, 1343, 1344, 1345, 2688, 4000, 5000, 100000], np.float64)
+    n, rows, k = len(top), 3, 64
+    x = np.rint(rng.uniform(-1, 1, (n, rows, k)) * top[:, None, None])
+    x[:, 0, 0] = top
+    x = (x * 2.0 ** -149).astype(np.float32)
+    xt = torch.from_numpy(x).cuda()
+    g = torch.empty(n, dtype=torch.float32, device="cuda")
+    m.moe_fp4_global_scale(n, rows, k, xt, g)
+    steps = np.rint(top / 2688)  # in units of 2^-149; halves go to the even one
+    assert np.array_equal(g.cpu().numpy().astype(np.float64) * 2.0 ** 149, np.maximum(steps, 1))
+    codes = torch.empty((n, rows, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n, rows, k // 16), dtype=torch.uint8, device="cuda")
+    y = torch.empty((n, rows, k), dtype=torch.float32, device="cuda")
+    m.moe_quantize_fp4(m.MOE_WDTYPE_NVFP4, n, rows, k, xt, g, codes, scales)
+    c, s = ref.nv_quantize(x, g.cpu().numpy())
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    m.moe_dequantize_fp4(m.MOE_WDTYPE_NVFP4, n, rows, k, codes, scales, g, y)
+    got = y.cpu().numpy()
+    assert np.isfinite(got).all()
+    assert np.array_equal(got, ref.nv_values(c, s, g.cpu().numpy()).astype(np.float32))
