@@ -220,7 +220,8 @@ MOE_API int moe_quantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_
                              const float* g, uint8_t* codes, uint8_t* scales, moe_stream_t stream);
 
 /* NVFP4 global scales: g[m] = amax(x[m]) / (6 * 448), rounded once, at least the
- * smallest fp32 number (2^-149); 1 for an all-zero matrix. x as for moe_quantize_fp4, k a multiple of 16. */
+ * smallest fp32 number (2^-149); 1 for an all-zero or empty (rows = 0) matrix. x as
+ * for moe_quantize_fp4, k a multiple of 16. */
 MOE_API int moe_fp4_global_scale(int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype, const void* x, float* g,
                                  moe_stream_t stream);
 

@@ -1004,7 +1004,7 @@ static int check_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, int
   if (n_mat < 0 || rows < 0 || k <= 0) return MOE_ERR_INVALID_ARG;
   if (k % (mx ? 32 : 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
   constexpr int64_t kMost = (int64_t)1 << 40;
-  if (rows > kMost / k || (rows && n_mat > kMost / (rows * k))) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows > kMost / k || n_mat > kMost / ((rows ? rows : 1) * k)) return MOE_ERR_UNSUPPORTED_SHAPE;
   *elems = rows * k;
   if (n_mat * *elems == 0) return MOE_OK;
   if (!x) return MOE_ERR_INVALID_ARG;
@@ -1027,7 +1027,7 @@ int moe_fp4_global_scale(int64_t n_mat, int64_t rows, int32_t k, int32_t x_dtype
                          moe_stream_t stream) {
   int64_t elems = 0;
   const int rc = check_fp4(MOE_WDTYPE_NVFP4, n_mat, rows, k, x_dtype, x, &elems);
-  if (rc != MOE_OK || n_mat * elems == 0) return rc;
+  if (rc != MOE_OK || n_mat == 0) return rc;
   if (!g) return MOE_ERR_INVALID_ARG;
   if (!aligned(g, 4)) return MOE_ERR_MISALIGNED;
   CUDA_TRY(launch_fp4_global_scale(x_dtype == MOE_VALUES_F32, n_mat, elems, x, g, reinterpret_cast<cudaStream_t>(stream)));

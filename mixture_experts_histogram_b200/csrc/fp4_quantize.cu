@@ -381,6 +381,8 @@ cudaError_t launch_quantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems,
 cudaError_t launch_fp4_global_scale(bool f32, int64_t n_mat, int64_t elems, const void* x, float* g, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(g, 0, (size_t)n_mat * 4, s);
   if (e != cudaSuccess) return e;
+  const dim3 each((unsigned)ceil_div(n_mat, kThreads));
+  if (elems == 0) return launch_pdl(global_scale_kernel, each, dim3(kThreads), 0, s, 1, n_mat, g);
   const int64_t vecs = elems / kVec;
   dim3 grid = step_grid(n_mat, vecs, f32 ? kAmaxSteps<float> : kAmaxSteps<__nv_bfloat16>);
   const unsigned most = (unsigned)ceil_div(kAmaxCtas, grid.y);
@@ -390,7 +392,7 @@ cudaError_t launch_fp4_global_scale(bool f32, int64_t n_mat, int64_t elems, cons
           : launch_pdl(amax_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, 1, n_mat, vecs,
                        static_cast<const __nv_bfloat16*>(x), gb);
   if (e != cudaSuccess) return e;
-  return launch_pdl(global_scale_kernel, dim3((unsigned)ceil_div(n_mat, kThreads)), dim3(kThreads), 0, s, 1, n_mat, g);
+  return launch_pdl(global_scale_kernel, each, dim3(kThreads), 0, s, 1, n_mat, g);
 }
 
 cudaError_t launch_dequantize_fp4(bool mx, bool f32, int64_t n_mat, int64_t elems, const uint8_t* codes,

@@ -164,3 +164,11 @@ def test_few_sizes_that_always_fit(lib):
                     assert call(w, T, H, I) == m.MOE_ERR_WORKSPACE_TOO_SMALL, (w, T, H, I)  # all else in order
         for H in (37888 // unit * unit + unit, 40960, 65536):
             assert call(w, 1, H, unit) == m.MOE_ERR_UNSUPPORTED_SHAPE, (w, H)
+
+
+def test_global_scale_of_empty_matrices_refusals(lib):
+    a = lib.moe_fp4_global_scale  # (n_mat, rows, k, x_dtype, x, g, stream)
+    assert a(0, 0, 32, 1, None, None, None) == a(0, 4, 32, 1, None, None, None) == m.MOE_OK
+    assert a(3, 0, 32, 1, None, None, None) == m.MOE_ERR_INVALID_ARG  # three scales to write
+    assert a(3, 0, 32, 1, None, 514, None) == m.MOE_ERR_MISALIGNED
+    assert a(1 << 40, 0, 32, 1, None, 512, None) == m.MOE_ERR_UNSUPPORTED_SHAPE

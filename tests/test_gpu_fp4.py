@@ -458,3 +458,11 @@ def test_nvfp4_tiniest_matrices(m):
     got = y.cpu().numpy()
     assert np.isfinite(got).all()
     assert np.array_equal(got, ref.nv_values(c, s, g.cpu().numpy()).astype(np.float32))
+
+
+def test_global_scale_of_empty_matrices(m):
+    """Matrices without rows have a scale too: that of zeros."""
+    import torch
+    g = torch.full((301,), float("nan"), device="cuda")
+    m.moe_fp4_global_scale(300, 0, 32, torch.empty((300, 0, 32), device="cuda"), g)
+    assert (g[:300] == 1).all() and torch.isnan(g[300])
