@@ -226,8 +226,10 @@ MOE_API int moe_fp4_global_scale(int64_t n_mat, int64_t rows, int32_t k, int32_t
                                  moe_stream_t stream);
 
 /* The values that codes and scales stand for: y [n_mat, rows, k] = (e2m1 x
- * scale) x g, rounded once to fp32 (MXFP4: exact in fp32) and, for y_dtype
- * MOE_VALUES_BF16, once more to bf16. Layouts as for moe_quantize_fp4. */
+ * scale) x g, rounded once to fp32 and, for y_dtype MOE_VALUES_BF16, once more to
+ * bf16. MXFP4 values are exact in fp32 but for those of 2^128 and more, which become
+ * infinite (codes of 4 and 6 with scale byte 253, of 2 to 6 with 254); moe_quantize_fp4
+ * makes no such bytes. Layouts as for moe_quantize_fp4. */
 MOE_API int moe_dequantize_fp4(int32_t format, int64_t n_mat, int64_t rows, int32_t k, const uint8_t* codes,
                                const uint8_t* scales, const float* g, int32_t y_dtype, void* y, moe_stream_t stream);
 

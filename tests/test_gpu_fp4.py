@@ -466,3 +466,17 @@ def test_global_scale_of_empty_matrices(m):
     g = torch.full((301,), float("nan"), device="cuda")
     m.moe_fp4_global_scale(300, 0, 32, torch.empty((300, 0, 32), device="cuda"), g)
     assert (g[:300] == 1).all() and torch.isnan(g[300])
+
+
+def test_mxfp4_every_scale_byte(m):
+    """Every E8M0 byte with every code: exact in fp32, infinite from 2^128 up, NaN for byte 255."""
+    import torch
+    codes = np.tile(np.arange(0, 256, 1, dtype=np.uint8).reshape(16, 16), (256, 1, 1))
+    scales = np.broadcast_to(np.arange(256, dtype=np.uint8)[:, None, None], (256, 16, 1)).copy()
+    y = torch.empty((256, 16, 32), dtype=torch.float32, device="cuda")
+    m.moe_dequantize_fp4(m.MOE_WDTYPE_MXFP4, 256, 16, 32, m.to_device(codes), m.to_device(scales), None, y)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = ref.mx_values(codes, scales).astype(np.float32)
+    got = y.cpu().numpy()
+    assert np.array_equal(got, want, equal_nan=True) and np.array_equal(np.isnan(got[255]), np.ones((16, 32), bool))
+    assert np.isinf(got[253:255]).any() and np.isfinite(got[:253]).all()
