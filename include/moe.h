@@ -158,11 +158,18 @@ MOE_API int moe_forward(const moe_config* cfg, int64_t T, const void* x, const m
  * moe_forward (bf16, or the storage's quantisation); each token's expert outputs
  * are gate-weighted and summed in fp32 without an intermediate rounding, by
  * ascending index and the shared expert last: a token's result does not depend on
- * the other tokens of the call. The tokens' activations must leave room for the
+ * the other tokens of the call. On 4-bit storage the activations are multiplied as f16
+ * next to one power of two for 128 inputs. That is exact for NVFP4 values down to 2^-31
+ * of the largest of their 128, and for MXFP4 blocks with scales down to 2^-35 of the
+ * largest of their four; smaller ones lose bits and, from 2^-39 and 2^-37 down, vanish
+ * (moe_forward keeps them; in the sums they count only where the weights of the larger
+ * ones are as much smaller). MXFP4 weight scales above 2^100 may overflow here.
+ * The tokens' activations must leave room for the
  * weight ring in shared memory, and a CTA's share of the outputs for their sums
  * (MOE_ERR_UNSUPPORTED_SHAPE otherwise): T * max(H, I) <= 65,536 with H <= 256 x the
- * number of SMs (37,888 on 148) always does. The cooperative launch starts when every SM is free: it
- * waits for kernels of other streams to end. One workspace serves one call at a time.
+ * number of SMs (37,888 on 148) always does. The cooperative launch starts when every
+ * SM is free: it waits for kernels of other streams to end. One workspace serves one
+ * call at a time.
  */
 enum { MOE_FEW_MAX_TOKENS = 8 };
 MOE_API int moe_forward_few(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w, void* out,

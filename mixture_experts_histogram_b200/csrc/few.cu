@@ -175,8 +175,8 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1,
 // (FP8; exact); or, for 4-bit weights, f16 next to a power of two for each 128 inputs:
 // NVFP4, whose activations are not quantised, with the largest at [2^14, 2^15); MXFP4,
 // whose quantised values have exponents of their own for each 32 inputs, with the
-// largest of these at 2^12. What f16 cannot hold then is below 2^-36 of the largest
-// value, where the fp32 sums have 24 bits. Values lie in input order, but for NVFP4,
+// largest of these at 2^12. What f16 cannot hold then is below 2^-31 (NVFP4 values) or
+// 2^-35 (MXFP4 blocks) of the largest, where the fp32 sums have 24 bits. Values lie in input order, but for NVFP4,
 // whose groups of 8 inputs are transposed 4 x 4 within 32 x 4 inputs, as its lanes
 // read them.
 template <int kW>

@@ -326,3 +326,39 @@ def test_few_workspace_of_a_larger_batch(m, w):
         m.moe_forward(call.cfg, T, x, call.w, again, call.ws)
         assert torch.equal(again.view(torch.int16), whole.view(torch.int16))
         assert (mem[nb:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("w", [2, 3], ids=lambda w: FMT[w])
+def test_few_small_activations_next_to_large_ones(m, w):
+    """4-bit storage, where 128 inputs share a power of two: activations at the stated distance below
+    the largest of their 128 (NVFP4 2^31, MXFP4 blocks 2^35), whose weights are zero, keep all bits."""
+    T, H, I, E, k, S = 3, 1024, 512, 6, 2, 1
+    wt, values, shared = host_weights(w, 95, E, S, H, I)
+    rng = np.random.default_rng(96)
+    big = np.zeros(H, bool)
+    if w == 2:
+        big[::128] = True
+        x = rng.integers(128, 256, (T, H)) * 2.0 ** -7 * rng.choice([-1.0, 1.0], (T, H))  # magnitudes in [1, 2)
+        x[:, big] = 1.5 * 2.0 ** 31
+    else:
+        big.reshape(-1, 32)[::4] = True
+        x = rng.choice([1.0, 1.5, 2.0, 3.0, 4.0, 6.0], (T, H)) * rng.choice([-1.0, 1.0], (T, H))
+        x[:, 33::32] = 6.0  # every block's largest: scale 1
+        x[:, big] = 6.0 * 2.0 ** 35
+    for pre in ("", "s"):
+        for name in "13":
+            c = wt[pre + "w" + name]
+            codes = np.stack((c & 15, c >> 4), -1).reshape(*c.shape[:-1], H)
+            codes[..., big] = 0
+            wt[pre + "w" + name] = (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+    wt["router_w"] = np.zeros_like(wt["router_w"])
+    wt["router_bias"] = np.arange(E, dtype=np.float32)
+    xh = synth.f32_to_bf16(x.astype(np.float32))
+    assert np.array_equal(synth.bf16_to_f32(xh), x.astype(np.float32))
+    e = np.exp([1.0, 0.0])
+    idx, gate = np.tile([E - 1, E - 2], (T, 1)), np.tile(e / e.sum(), (T, 1))
+    call = Call(m, w, T, H, I, E, k, S, wt)
+    got = bf16_bits_to_f64(bits(call(m.to_device(xh))))
+    want = ref.layer(FMT[w], x, idx, gate, values, shared)
+    assert m.moe_read_status(call.ws) == 0
+    assert rows_rel(got, want).max() < 1e-2
