@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
+            // (The leader's MMAs read these scales in both CTAs' tensor memory.)
             if (kPair) mbar_arrive_cluster(map_to_cta(&sfull[slot0 + half], 0));
             else mbar_arrive(&sfull[slot0 + half]);
           }
