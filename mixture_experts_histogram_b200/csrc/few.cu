@@ -378,6 +378,28 @@ __device__ __forceinline__ void line_mma(Sums& acc, const Operands& o, float sb0
   }
 }
 
+// What FP8 h is quantised with: its block's scale s as e4m3_scale gives it, and codes
+// (h up) r, with up = 2^64 where s or its reciprocal could leave the normal range, else 1.
+// Quotient and reciprocal are corrected by their residuals in fused arithmetic (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990) and
+// equal __fdiv_rn and __frcp_rn for every finite largest magnitude (an infinite one gives
+// NaN codes). With those two functions T = 8 took 4% longer, T = 1 0.5 us.
+struct HScale {
+  float s, up, r;
+  __device__ __forceinline__ explicit HScale(float amax) {
+    constexpr float c = 1.0f / 448.0f;
+    const bool small = amax < 0x1p-60f;
+    up = small ? kE4m3Lift : 1.0f;
+    const float a = amax * up, q = a * c;
+    s = fmaf(fmaf(-q, 448.0f, a), c, q);
+    if (small) s = amax > 0.0f ? fmaxf(s * (1.0f / kE4m3Lift), 0x1p-149f) : 1.0f;
+    if (!(amax <= INFINITY)) s = 1.0f;  // a NaN among the values: its code is NaN
+    const float b = s * up;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+    r = fmaf(r, fmaf(-b, r, 1.0f), r);
+  }
+};
+
 // 8 values of a row (inputs 8 v .. 8 v + 7; all lanes of the warp take part, `live`
 // ones hold values) into the operand row at `row` with scales behind it. FP8:
 // kDivide quantises by quotients (x, as moe_quantize_act defines it), else by products
@@ -406,13 +428,12 @@ __device__ __forceinline__ void store_operand(uint8_t* row, int scales_at, int v
     if constexpr (kW == MOE_WDTYPE_FP8_E4M3) {
       // (A NaN fails the comparison, keeps scale 1 and becomes a NaN code.)
       const float amax = __uint_as_float(m);
-      s = e4m3_scale(amax);
-      const float up = !kDivide && e4m3_tiny(s) ? kE4m3Lift : 1.0f;
-      const float r = kDivide ? 1.0f : __frcp_rn(s * up);
+      const HScale hs(amax);
+      s = kDivide ? e4m3_scale(amax) : hs.s;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 q = kDivide ? make_float2(__fdiv_rn(f[2 * j], s), __fdiv_rn(f[2 * j + 1], s))
-                                 : make_float2(f[2 * j] * up * r, f[2 * j + 1] * up * r);
+                                 : make_float2(f[2 * j] * hs.up * hs.r, f[2 * j + 1] * hs.up * hs.r);
         h[j] = f16x2_of_e4m3x2(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
       }
     } else if constexpr (kW == MOE_WDTYPE_MXFP4) {

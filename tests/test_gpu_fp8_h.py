@@ -111,3 +111,17 @@ def test_tiny_tokens_stay_finite(m, variant, size):  # noqa: F811
     if size > 1e-21:
         want = ref.layer("fp8", synth.bf16_to_f32(xh).astype(np.float64), idx, gate, of(""), of("s"))
         assert max(rows_rel(out, want).max() for out in outs) < 2e-2
+
+
+def test_infinite_h_is_not_lost(m, variant):  # noqa: F811
+    """Finite tokens whose h overflows to infinity give rows that are not finite; others keep theirs."""
+    xh, wt = tie_layer(3)
+    call = Call(m, 1, T, H, I, E, 1, 0, wt)
+    x = m.to_device(xh)
+    few, whole = bits(call(x)).copy(), bits(forward(m, call, x)).copy()
+    wt["s1"][[2, 5]], wt["s3"][[2, 5]] = 2.0 ** 70, 2.0 ** 70
+    call = Call(m, 1, T, H, I, E, 1, 0, wt)
+    for got, want in ((bits(call(x)).copy(), few), (bits(forward(m, call, x)), whole)):
+        keep = [t for t in range(T) if t not in (2, 5)]
+        assert np.array_equal(got[keep], want[keep])
+        assert not np.isfinite(bf16_bits_to_f64(got[[2, 5]])).any()
