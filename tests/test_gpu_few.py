@@ -362,3 +362,24 @@ def test_few_small_activations_next_to_large_ones(m, w):
     want = ref.layer(FMT[w], x, idx, gate, values, shared)
     assert m.moe_read_status(call.ws) == 0
     assert rows_rel(got, want).max() < 1e-2
+
+
+@pytest.mark.parametrize("w", [0, 1, 2, 3], ids=lambda w: FMT[w])
+@pytest.mark.parametrize("T,H,I,E,k,S", [(1, 37888, 512, 2, 1, 1), (1, 512, 65536, 2, 2, 0), (2, 32768, 512, 3, 2, 0),
+                                         (4, 512, 16384, 3, 2, 0)])
+def test_few_largest_layers(m, w, T, H, I, E, k, S):
+    """The ends of the sizes that always fit: 256 output rows a CTA, one row of h at a time."""
+    import torch
+    wt, values, shared = host_weights(w, 97, E, S, H, I)
+    xh = synth.normal_bf16(98, 1, (T, H), 1.0)
+    idx_r, gate_r, logits_r = oracle.route(xh, wt["router_w"], None, k, want_logits=True)
+    call = Call(m, w, T, H, I, E, k, S, wt)
+    x = m.to_device(xh)
+    got = bits(call(x)).copy()
+    assert m.moe_read_status(call.ws) == 0
+    check_routing(call.idx.cpu().numpy(), call.gate.cpu().numpy(), logits_r, idx_r, gate_r)
+    toks = np.flatnonzero(unique_tokens(logits_r, k))
+    want = ref.layer(FMT[w], synth.bf16_to_f32(xh).astype(np.float64), idx_r, gate_r, values, shared, toks)
+    assert rows_rel(bf16_bits_to_f64(got)[toks], want).max() < (2e-2 if w == 1 else 1e-2)
+    for _ in range(50):
+        assert torch.equal(call(x).view(torch.int16).cpu(), torch.from_numpy(got.view(np.int16)))
