@@ -33,12 +33,12 @@
 // MMAs are far from a limit, and 8 columns fit 8 tokens without padding.
 //
 // Measured (H = 4096, I = 1536, 352 experts, top-8 and a shared one, in long runs under
-// the power limit; the floor is the weights at 6.45 TB/s): BF16 T = 3 159 us (0.91 of the
-// floor's rate), FP8 T = 8 234 us (0.75; 212 us in short runs at full clocks), T = 1 47 us
+// the power limit; the floor is the weights at 6.45 TB/s): BF16 T = 3 153 us (0.94 of the
+// floor's rate), FP8 T = 8 224 us (0.79; 212 us in short runs at full clocks), T = 1 47 us
 // (0.57: of these the logits, the cooperative launch and the selection take 8 us, the
 // first tile 3 and the barrier 4). 4-bit storage is bound by the expansion of the codes,
 // about 370 warp instructions for a 2 KB line of 16 rows: MXFP4 T = 8 216 us (0.44), T = 1
-// 49 us; NVFP4 T = 5 149 us (0.44). Twelve multiplying warps instead of eight leave 96
+// 49 us; NVFP4 T = 5 144 us (0.45). Twelve multiplying warps instead of eight leave 96
 // registers each: MXFP4 T = 8 242 us; the halves of a line as a rolled loop: 230 us, two
 // lines unrolled: 288 us.
 #include <cuda_bf16.h>
